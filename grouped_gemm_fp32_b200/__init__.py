@@ -17,4 +17,8 @@ from ._lib import (MOE_GEMM1, MOE_GEMM2, MoeDims, MoeError, grouped_gemm_bwd_dw,
                    moe_workspace_size, MOE_EP_MAX_WORLD, MOE_EP_WAIT_DX, MOE_EP_WAIT_Y,
                    MoeEpPeers, grouped_gemm_bwd_dx_ep, grouped_gemm_fwd_ep, moe_ep_combine_bwd,
                    moe_ep_dispatch, moe_ep_plan, moe_ep_wait, moe_ep_workspace_size,
-                   moe_ep_zero_pads)
+                   moe_ep_zero_pads, GradList, MoeGrad, MoeNormCfg, MoeRouteCfg, MOE_BF16, MOE_F16,
+                   MOE_F32, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, moe_block_norm,
+                   moe_block_norm_bwd, moe_gate_bwd, moe_gate_logits, moe_grad_clip,
+                   moe_grad_clip_norm, moe_grad_norm, moe_grad_workspace_size,
+                   moe_norm_workspace_size, moe_route_bwd, moe_route_topk)

@@ -27,9 +27,14 @@ EXPORTS = (
     "moe_status_string", "moe_last_cuda_error",
     "moe_ep_workspace_size", "moe_ep_plan", "moe_ep_dispatch", "moe_ep_zero_pads", "moe_ep_wait",
     "moe_ep_combine_bwd", "grouped_gemm_fwd_ep", "grouped_gemm_bwd_dx_ep",
+    "moe_gate_logits", "moe_route_topk", "moe_route_bwd", "moe_gate_bwd",
+    "moe_block_norm", "moe_block_norm_bwd", "moe_norm_workspace_size",
+    "moe_grad_norm", "moe_grad_clip", "moe_grad_clip_norm", "moe_grad_workspace_size",
 )
 MOE_EP_MAX_WORLD = 8
 MOE_EP_WAIT_Y, MOE_EP_WAIT_DX = 3, 5
+MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 
 class MoeError(RuntimeError):
@@ -75,6 +80,36 @@ class MoeEpPeers(ctypes.Structure):
         return p
 
 
+class MoeRouteCfg(ctypes.Structure):
+    """Mirror of ``struct moe_route_cfg``: how a router scores and chooses."""
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+    @classmethod
+    def of(cls, score="softmax", n_group=1, topk_group=1, group_top=2, renorm=True, scale=1.0):
+        """``score``: "softmax", "sigmoid" or one of the MOE_SCORE_ values."""
+        score = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}.get(score, score)
+        return cls(int(score), int(n_group), int(topk_group), int(group_top), int(bool(renorm)),
+                   float(scale))
+
+
+class MoeNormCfg(ctypes.Structure):
+    """Mirror of ``struct moe_norm_cfg``: the numbers of a block boundary."""
+    _fields_ = [("eps", ctypes.c_float), ("res_scale", ctypes.c_float),
+                ("block_scale", ctypes.c_float), ("seq_len", ctypes.c_int64)]
+
+    @classmethod
+    def of(cls, eps=1e-6, res_scale=1.0, block_scale=1.0, seq_len=0):
+        return cls(float(eps), float(res_scale), float(block_scale), int(seq_len))
+
+
+class MoeGrad(ctypes.Structure):
+    """Mirror of ``struct moe_grad``: one tensor of a gradient list."""
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("type", ctypes.c_int32)]
+
+
 def lib_path() -> str:
     return _LIB_PATH
 
@@ -90,6 +125,7 @@ def load():
     lib = ctypes.CDLL(_LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
     D = ctypes.POINTER(MoeDims)
+    R, N = ctypes.POINTER(MoeRouteCfg), ctypes.POINTER(MoeNormCfg)
     sig = {
         "moe_rows_routed": (i64, [D]),
         "moe_rows_total": (i64, [D]),
@@ -124,6 +160,18 @@ def load():
                                       vp, vp]),
         "grouped_gemm_bwd_dx_ep": (i32, [D, vp, ctypes.POINTER(MoeEpPeers), i32, vp, vp, vp, vp,
                                          vp, vp]),
+        "moe_gate_logits": (i32, [D, vp, vp, vp, vp, sz, vp]),
+        "moe_route_topk": (i32, [D, R, i32, vp, vp, vp, vp, vp, vp]),
+        "moe_route_bwd": (i32, [D, R, i32, vp, vp, vp, vp, vp, i64, vp, vp]),
+        "moe_gate_bwd": (i32, [D, vp, vp, vp, vp, vp, i32, vp, sz, vp]),
+        "moe_block_norm": (i32, [D, N, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "moe_norm_workspace_size": (sz, [D, N]),
+        "moe_block_norm_bwd": (i32, [D, N, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                     i32, vp, sz, vp]),
+        "moe_grad_workspace_size": (sz, [i64]),
+        "moe_grad_norm": (i32, [vp, i64, i32, vp, vp, vp, sz, vp]),
+        "moe_grad_clip": (i32, [vp, i64, vp, ctypes.c_float, vp, vp, vp]),
+        "moe_grad_clip_norm": (i32, [vp, i64, ctypes.c_float, vp, vp, vp, vp, sz, vp]),
         "moe_status_string": (ctypes.c_char_p, [i32]),
         "moe_last_cuda_error": (ctypes.c_char_p, []),
     }
@@ -332,3 +380,203 @@ def grouped_gemm_bwd_dx_ep(dims, ws, peers, which, dy_recv, dy_shared, w, a1, ou
     _ck(load().grouped_gemm_bwd_dx_ep(ctypes.byref(dims), _p(ws), ctypes.byref(peers), int(which),
                                       _p(dy_recv), _p(dy_shared), _p(w), _p(a1), _p(out),
                                       _s(stream)), "grouped_gemm_bwd_dx_ep")
+
+
+# ---------------------------------------------------- routers of other kinds --
+# The calls below read a tensor's element type from its dtype, so they check what
+# they are given: dtype, element count, contiguity and that the tensor is on the
+# current device.  Integer addresses pass unchecked, as in the calls above.
+_TYPES: dict = {}
+
+
+def _types():
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16})
+        _TYPES.update(f32=torch.float32, i32=torch.int32, bf16=torch.bfloat16, u8=torch.uint8,
+                      f64=torch.float64, device=torch.cuda.current_device)
+    return _TYPES
+
+
+def _need(what, t, dtype, numel, dev):
+    """Device pointer of a tensor after its checks; NULL for None."""
+    if t is None or type(t) is int:
+        return t
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {t.dtype} given, {dtype} needed")
+    if t.numel() != numel:
+        raise ValueError(f"{what}: shape {tuple(t.shape)} has {t.numel()} elements, {numel} needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: not contiguous (strides {t.stride()})")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, the current device is cuda:{dev}")
+    return t.data_ptr()
+
+
+def _kind(what, t, allowed):
+    """MOE_ type of a tensor."""
+    ty = _types().get(getattr(t, "dtype", None))
+    if ty not in allowed:
+        raise ValueError(f"{what}: unsupported element type {getattr(t, 'dtype', type(t))}")
+    return ty
+
+
+def _bytes(what, ws, dev):
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"{what}: a contiguous tensor on cuda:{dev} is needed")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def moe_gate_logits(dims, x, wg, logits, ws, stream=None):
+    y = _types()
+    dev = y["device"]()
+    T, d, E = dims.T, dims.d, dims.E
+    _ck(load().moe_gate_logits(ctypes.byref(dims), _need("x", x, y["bf16"], T * d, dev),
+                               _need("wg", wg, y["f32"], E * d, dev),
+                               _need("logits", logits, y["f32"], T * E, dev),
+                               *_bytes("ws", ws, dev), _s(stream)), "moe_gate_logits")
+
+
+def moe_route_topk(dims, cfg, logits, bias, topk_idx, topk_w, probs, stream=None):
+    y = _types()
+    dev, f32 = y["device"](), y["f32"]
+    T, E, k = dims.T, dims.E, dims.k
+    kind = _kind("logits", logits, (MOE_F32, MOE_BF16))
+    _ck(load().moe_route_topk(ctypes.byref(dims), ctypes.byref(cfg), kind,
+                              _need("logits", logits, logits.dtype, T * E, dev),
+                              _need("bias", bias, f32, E, dev),
+                              _need("topk_idx", topk_idx, y["i32"], T * k, dev),
+                              _need("topk_w", topk_w, f32, T * k, dev),
+                              _need("probs", probs, f32, T * E, dev), _s(stream)),
+        "moe_route_topk")
+
+
+def moe_route_bwd(dims, cfg, logits, topk_idx, topk_w, dw, seq_grad, seq_len, dlogits,
+                  stream=None):
+    y = _types()
+    dev, f32 = y["device"](), y["f32"]
+    T, E, k = dims.T, dims.E, dims.k
+    kind = _kind("logits", logits, (MOE_F32, MOE_BF16))
+    seq_len = int(seq_len)
+    rows = -(-T // seq_len) if seq_grad is not None and seq_len > 0 else 0
+    if rows and type(seq_grad) is not int and seq_grad.numel() > rows * E:
+        seq_grad = seq_grad.view(-1)[:rows * E]     # MoEBuffers.bal_grad holds more rows
+    _ck(load().moe_route_bwd(ctypes.byref(dims), ctypes.byref(cfg), kind,
+                             _need("logits", logits, logits.dtype, T * E, dev),
+                             _need("topk_idx", topk_idx, y["i32"], T * k, dev),
+                             _need("topk_w", topk_w, f32, T * k, dev),
+                             _need("dw", dw, f32, T * k, dev),
+                             _need("seq_grad", seq_grad, f32, rows * E, dev), seq_len,
+                             _need("dlogits", dlogits, logits.dtype, T * E, dev), _s(stream)),
+        "moe_route_bwd")
+
+
+def moe_gate_bwd(dims, x, wg, dlogits, dx, dwg, accumulate, ws, stream=None):
+    y = _types()
+    dev, f32 = y["device"](), y["f32"]
+    T, d, E = dims.T, dims.d, dims.E
+    _ck(load().moe_gate_bwd(ctypes.byref(dims), _need("x", x, y["bf16"], T * d, dev),
+                            _need("wg", wg, f32, E * d, dev),
+                            _need("dlogits", dlogits, f32, T * E, dev),
+                            _need("dx", dx, y["bf16"], T * d, dev),
+                            _need("dwg", dwg, f32, E * d, dev), int(accumulate),
+                            *_bytes("ws", ws, dev), _s(stream)), "moe_gate_bwd")
+
+
+# ------------------------------------------------------------- block norms --
+def _gate_rows(dims, cfg) -> int:
+    return max(1, -(-dims.T // cfg.seq_len)) if cfg.seq_len > 0 else 1
+
+
+def moe_block_norm(dims, cfg, y, res, w_post, gate, w_pre, res_out, n, stream=None):
+    ty = _types()
+    dev, f32, bf = ty["device"](), ty["f32"], ty["bf16"]
+    d, m = dims.d, dims.T * dims.d
+    kind = _kind("res", res, (MOE_F32, MOE_BF16))
+    _ck(load().moe_block_norm(ctypes.byref(dims), ctypes.byref(cfg), kind,
+                              _need("y", y, bf, m, dev), _need("res", res, res.dtype, m, dev),
+                              _need("w_post", w_post, f32, d, dev),
+                              _need("gate", gate, f32, _gate_rows(dims, cfg) * d, dev),
+                              _need("w_pre", w_pre, f32, d, dev),
+                              _need("res_out", res_out, res.dtype, m, dev),
+                              _need("n", n, bf, m, dev), _s(stream)), "moe_block_norm")
+
+
+def moe_norm_workspace_size(dims, cfg) -> int:
+    return int(load().moe_norm_workspace_size(ctypes.byref(dims), ctypes.byref(cfg)))
+
+
+def moe_block_norm_bwd(dims, cfg, dn, dres_out, y, u, w_post, gate, w_pre, dy, dres, dw_post,
+                       dgate, dw_pre, accumulate, ws, stream=None):
+    ty = _types()
+    dev, f32, bf = ty["device"](), ty["f32"], ty["bf16"]
+    d, m, g = dims.d, dims.T * dims.d, _gate_rows(dims, cfg) * dims.d
+    kind = _kind("dres", dres, (MOE_F32, MOE_BF16))
+    rt = dres.dtype
+    _ck(load().moe_block_norm_bwd(ctypes.byref(dims), ctypes.byref(cfg), kind,
+                                  _need("dn", dn, bf, m, dev),
+                                  _need("dres_out", dres_out, rt, m, dev),
+                                  _need("y", y, bf, m, dev), _need("u", u, rt, m, dev),
+                                  _need("w_post", w_post, f32, d, dev),
+                                  _need("gate", gate, f32, g, dev),
+                                  _need("w_pre", w_pre, f32, d, dev), _need("dy", dy, bf, m, dev),
+                                  _need("dres", dres, rt, m, dev),
+                                  _need("dw_post", dw_post, f32, d, dev),
+                                  _need("dgate", dgate, f32, g, dev),
+                                  _need("dw_pre", dw_pre, f32, d, dev), int(accumulate),
+                                  *_bytes("ws", ws, dev), _s(stream)), "moe_block_norm_bwd")
+
+
+# ---------------------------------------------------------- gradient clipping --
+class GradList:
+    """The tensors of a gradient norm and clipping as the array the library reads,
+    built once for tensors that stay where they are.  ``outs``: where the clipped
+    gradients go (None, or None entries: in place).  Keeps the tensors alive."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = [None] * len(self.grads) if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients, {len(self.outs)} outs")
+        self.array = (MoeGrad * max(1, len(self.grads)))()
+        dev = _types()["device"]() if self.grads else 0
+        for a, g, o in zip(self.array, self.grads, self.outs):
+            a.type = _kind("gradient", g, (MOE_F32, MOE_BF16, MOE_F16))
+            a.data = _need("gradient", g, g.dtype, g.numel(), dev)
+            a.out = _need("clipped gradient", o, g.dtype, g.numel(), dev)
+            a.n = g.numel()
+
+    def __len__(self):
+        return len(self.grads)
+
+
+def moe_grad_workspace_size(n_grads) -> int:
+    return int(load().moe_grad_workspace_size(int(n_grads)))
+
+
+def moe_grad_norm(grads, accumulate, sumsq, norm, ws, stream=None):
+    y = _types()
+    dev = y["device"]()
+    _ck(load().moe_grad_norm(ctypes.addressof(grads.array), len(grads), int(accumulate),
+                             _need("sumsq", sumsq, y["f64"], 1, dev),
+                             _need("norm", norm, y["f32"], 1, dev), *_bytes("ws", ws, dev),
+                             _s(stream)), "moe_grad_norm")
+
+
+def moe_grad_clip(grads, sumsq, max_norm, norm, coef, stream=None):
+    y = _types()
+    dev = y["device"]()
+    _ck(load().moe_grad_clip(ctypes.addressof(grads.array), len(grads),
+                             _need("sumsq", sumsq, y["f64"], 1, dev), float(max_norm),
+                             _need("norm", norm, y["f32"], 1, dev),
+                             _need("coef", coef, y["f32"], 1, dev), _s(stream)), "moe_grad_clip")
+
+
+def moe_grad_clip_norm(grads, max_norm, sumsq, norm, coef, ws, stream=None):
+    y = _types()
+    dev = y["device"]()
+    _ck(load().moe_grad_clip_norm(ctypes.addressof(grads.array), len(grads), float(max_norm),
+                                  _need("sumsq", sumsq, y["f64"], 1, dev),
+                                  _need("norm", norm, y["f32"], 1, dev),
+                                  _need("coef", coef, y["f32"], 1, dev), *_bytes("ws", ws, dev),
+                                  _s(stream)), "moe_grad_clip_norm")

@@ -41,7 +41,8 @@
 //   all warps        routing, eight lanes per token (four tokens per warp at a
 //                    time): softmax (max-subtracted, expf), s = p + bias, k rounds of
 //                    a shuffle arg-max within the token's lanes (equal s -> lower
-//                    index), the renormalised weights
+//                    index), the renormalised weights; moe_gate_logits stores the logits
+//                    instead
 // With fewer 128-token tiles than half the SMs (T <= 9472 on 148 SMs) each tile
 // runs on a cluster pair instead: CTA 0 takes the first half of the K blocks,
 // CTA 1 the second, and after an exchange of partial logits through distributed
@@ -72,6 +73,7 @@ struct GateArgs {
   int32_t* topk_idx;
   float* topk_w;
   float* probs;
+  float* logits;  // set: the logits are written here and no token is routed
   int64_t T;
   int d, E, e_pad, k, stages;
   uint32_t stage_bytes, tmem_cols, idesc, idesc2;
@@ -431,7 +433,12 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
     }
     __syncthreads();
   }
-  if (!aborted) {
+  if (!aborted && a.logits != nullptr) {
+    for (int i = threadIdx.x; i < rows * a.E; i += blockDim.x) {
+      const int64_t t = m0 + r0 + i / a.E;
+      if (t < a.T) a.logits[t * a.E + i % a.E] = L[(r0 + i / a.E) * LS + i % a.E];
+    }
+  } else if (!aborted) {
     if (a.E <= 128)
       route_tile<16>(L + r0 * LS, LS, m0 + r0, rows, a.T, a.E, a.k, a.bias, a.topk_idx,
                      a.topk_w, a.probs);
@@ -460,7 +467,8 @@ int launch_split_wg(const moe_dims& dm, const float* wg, void* planes, void* str
 }
 
 int launch_gate_topk(const moe_dims& dm, const void* x, const float* wg, const float* bias,
-                     int32_t* idx, float* w, float* probs, void* ws, void* stream) {
+                     int32_t* idx, float* w, float* probs, float* logits, void* ws,
+                     void* stream) {
   const int64_t T = dm.T;
   if (T == 0) return MOE_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -480,6 +488,7 @@ int launch_gate_topk(const moe_dims& dm, const void* x, const float* wg, const f
   a.topk_idx = idx;
   a.topk_w = w;
   a.probs = probs;
+  a.logits = logits;
   a.T = T;
   a.d = dm.d;
   a.E = dm.E;

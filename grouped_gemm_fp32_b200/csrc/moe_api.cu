@@ -3,6 +3,8 @@
 // (except moe_get_device_status), nothing but plain pointers and sizes.
 #include <cuda_runtime.h>
 
+#include <initializer_list>
+
 #include "ep_internal.cuh"
 #include "moe_internal.cuh"
 
@@ -73,7 +75,7 @@ int moe_gate_topk(const moe_dims* dims, const void* x, const float* wg, const fl
   if (dims->E % 8) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!ws || ws_bytes < ws_layout(*dims).total) return MOE_ERR_INVALID_ARG;
   if (dims->T > 0 && (!x || !wg || !topk_idx || !topk_w)) return MOE_ERR_INVALID_ARG;
-  return launch_gate_topk(*dims, x, wg, bias, topk_idx, topk_w, probs, ws, stream);
+  return launch_gate_topk(*dims, x, wg, bias, topk_idx, topk_w, probs, nullptr, ws, stream);
 }
 
 int moe_router_bwd(const moe_dims* dims, const void* x, const float* wg, const float* probs,
@@ -115,6 +117,191 @@ int moe_seq_balance_loss(const moe_dims* dims, int64_t seq_len, float alpha,
   if (!ws || ws_bytes < ws_layout(*dims).total || !loss) return MOE_ERR_INVALID_ARG;
   if (dims->T > 0 && (!topk_idx || !probs || !seq_grad)) return MOE_ERR_INVALID_ARG;
   return launch_seq_balance(*dims, seq_len, alpha, topk_idx, probs, loss, seq_grad, ws, stream);
+}
+
+int moe_gate_logits(const moe_dims* dims, const void* x, const float* wg, float* logits, void* ws,
+                    size_t ws_bytes, void* stream) {
+  int rc = check_shape(dims, false);
+  if (rc) return rc;
+  if (dims->E % 8) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!ws || ws_bytes < ws_layout(*dims).total) return MOE_ERR_INVALID_ARG;
+  if (dims->T > 0 && (!x || !wg || !logits)) return MOE_ERR_INVALID_ARG;
+  return launch_gate_topk(*dims, x, wg, nullptr, nullptr, nullptr, nullptr, logits, ws, stream);
+}
+
+int moe_gate_bwd(const moe_dims* dims, const void* x, const float* wg, const float* dlogits,
+                 void* dx, float* dwg, int accumulate, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_shape(dims, false);
+  if (rc) return rc;
+  if (dims->E % 8) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!ws || ws_bytes < ws_layout(*dims).total || !wg || !dwg) return MOE_ERR_INVALID_ARG;
+  if (dims->T > 0 && (!x || !dlogits || !dx)) return MOE_ERR_INVALID_ARG;
+  return launch_gate_bwd(*dims, x, wg, dlogits, dx, dwg, accumulate ? 1 : 0, ws, stream);
+}
+
+// Shape and settings of a router (include/moe.h); only T, E and k of dims count.
+static int check_route(const moe_dims* dims, const moe_route_cfg* c, int type) {
+  if (!dims || !c || dims->T < 0 || dims->E <= 0 || dims->k <= 0) return MOE_ERR_INVALID_ARG;
+  if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (type != MOE_F32 && type != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->group_top != 1 && c->group_top != 2) return MOE_ERR_INVALID_ARG;
+  if (c->renorm != 0 && c->renorm != 1) return MOE_ERR_INVALID_ARG;
+  if (c->n_group < 1 || c->topk_group < 1 || c->topk_group > c->n_group)
+    return MOE_ERR_INVALID_ARG;
+  if (!(c->scale - c->scale == 0.0f)) return MOE_ERR_INVALID_ARG;  // not finite
+  if (dims->E > 256 || dims->k > dims->E || dims->T * dims->k >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (dims->E % c->n_group) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // a group must hold group_top experts, the kept groups k of them
+  const int size = dims->E / c->n_group;
+  if (c->n_group > 1 && (size < c->group_top || size * c->topk_group < dims->k))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+int moe_route_topk(const moe_dims* dims, const moe_route_cfg* cfg, int logits_type,
+                   const void* logits, const float* bias, int32_t* topk_idx, float* topk_w,
+                   float* probs, void* stream) {
+  const int rc = check_route(dims, cfg, logits_type);
+  if (rc) return rc;
+  if (dims->T > 0 && (!logits || !topk_idx || !topk_w)) return MOE_ERR_INVALID_ARG;
+  return launch_route_topk(*dims, *cfg, logits_type, logits, bias, topk_idx, topk_w, probs,
+                           stream);
+}
+
+int moe_route_bwd(const moe_dims* dims, const moe_route_cfg* cfg, int logits_type,
+                  const void* logits, const int32_t* topk_idx, const float* topk_w,
+                  const float* dw, const float* seq_grad, int64_t seq_len, void* dlogits,
+                  void* stream) {
+  const int rc = check_route(dims, cfg, logits_type);
+  if (rc) return rc;
+  if (dims->T > 0 && (!logits || !topk_idx || !topk_w || !dw || !dlogits))
+    return MOE_ERR_INVALID_ARG;
+  if (seq_grad && seq_len < 1) return MOE_ERR_INVALID_ARG;
+  return launch_route_bwd(*dims, *cfg, logits_type, logits, topk_idx, topk_w, dw, seq_grad,
+                          seq_len, dlogits, stream);
+}
+
+// Shape and settings of a block norm: rows of d % 64 == 0 up to 16384 columns.
+static int check_norm(const moe_dims* dims, const moe_norm_cfg* c) {
+  if (!dims || !c || dims->T < 0 || dims->d <= 0 || c->seq_len < 0) return MOE_ERR_INVALID_ARG;
+  if (!(c->eps > 0.0f) || !(c->eps - c->eps == 0.0f) ||
+      !(c->res_scale - c->res_scale == 0.0f) || !(c->block_scale - c->block_scale == 0.0f))
+    return MOE_ERR_INVALID_ARG;
+  if (dims->d % 64 || dims->d > 16384 || dims->T >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+// 16-byte aligned, as the vector accesses of the block norms need (NULL passes).
+static bool aligned16(std::initializer_list<const void*> p) {
+  for (const void* q : p)
+    if (reinterpret_cast<uintptr_t>(q) & 15) return false;
+  return true;
+}
+
+int moe_block_norm(const moe_dims* dims, const moe_norm_cfg* cfg, int res_type, const void* y,
+                   const void* res, const float* w_post, const float* gate, const float* w_pre,
+                   void* res_out, void* n, void* stream) {
+  const int rc = check_norm(dims, cfg);
+  if (rc) return rc;
+  if (res_type != MOE_F32 && res_type != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (dims->T == 0) return MOE_OK;  // tensors without elements may be NULL
+  if (!res || (w_pre == nullptr) != (n == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (y ? !res_out : (w_post || gate || res_out || !n)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16({y, res, w_post, gate, w_pre, res_out, n})) return MOE_ERR_INVALID_ARG;
+  NormArgs a{};
+  a.y = y;
+  a.res = res;
+  a.w_post = w_post;
+  a.gate = gate;
+  a.w_pre = w_pre;
+  a.u = res_out;
+  a.n = n;
+  return launch_block_norm(*dims, *cfg, res_type, a, stream);
+}
+
+size_t moe_norm_workspace_size(const moe_dims* dims, const moe_norm_cfg* cfg) {
+  return check_norm(dims, cfg) == MOE_OK ? norm_ws_bytes(*dims, *cfg) : 0;
+}
+
+int moe_block_norm_bwd(const moe_dims* dims, const moe_norm_cfg* cfg, int res_type,
+                       const void* dn, const void* dres_out, const void* y, const void* u,
+                       const float* w_post, const float* gate, const float* w_pre, void* dy,
+                       void* dres, float* dw_post, float* dgate, float* dw_pre, int accumulate,
+                       void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_norm(dims, cfg);
+  if (rc) return rc;
+  if (res_type != MOE_F32 && res_type != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
+  if (dims->T > 0) {  // without tokens the tensors of T rows may be NULL
+    if (dn ? (!w_pre || !u) : (w_pre || !dres_out)) return MOE_ERR_INVALID_ARG;
+    if (y ? !dy : (w_post || gate || dy)) return MOE_ERR_INVALID_ARG;
+    if (!dres) return MOE_ERR_INVALID_ARG;
+  }
+  if ((dw_post && !w_post) || (dgate && !gate) || (dw_pre && !w_pre)) return MOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < norm_ws_bytes(*dims, *cfg)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16({dn, dres_out, y, u, w_post, gate, w_pre, dy, dres, dw_post, dgate, dw_pre, ws}))
+    return MOE_ERR_INVALID_ARG;
+  NormArgs a{};
+  a.y = y;
+  a.res = u;
+  a.w_post = w_post;
+  a.gate = gate;
+  a.w_pre = w_pre;
+  a.dn = dn;
+  a.du = dres_out;
+  a.dy = dy;
+  a.dres = dres;
+  a.dw_post = dw_post;
+  a.dgate = dgate;
+  a.dw_pre = dw_pre;
+  a.accumulate = accumulate;
+  a.ws = ws;
+  return launch_block_norm_bwd(*dims, *cfg, res_type, a, stream);
+}
+
+// A list of gradient tensors: types, sizes and element alignment.
+static int check_grads(const moe_grad* g, int64_t n) {
+  if (n < 0 || (n > 0 && !g)) return MOE_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < n; ++i) {
+    if (g[i].type != MOE_F32 && g[i].type != MOE_BF16 && g[i].type != MOE_F16)
+      return MOE_ERR_INVALID_ARG;
+    const uintptr_t mask = g[i].type == MOE_F32 ? 3 : 1;
+    if (g[i].n < 0 || (g[i].n > 0 && !g[i].data)) return MOE_ERR_INVALID_ARG;
+    if (((uintptr_t)g[i].data | (uintptr_t)g[i].out) & mask) return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+size_t moe_grad_workspace_size(int64_t n_grads) { return n_grads < 0 ? 0 : grad_ws_bytes(n_grads); }
+
+int moe_grad_norm(const moe_grad* grads, int64_t n_grads, int accumulate, double* sumsq,
+                  float* norm, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_grads(grads, n_grads);
+  if (rc) return rc;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
+  if (!sumsq || !ws || ws_bytes < grad_ws_bytes(n_grads)) return MOE_ERR_INVALID_ARG;
+  return launch_grad_norm(grads, n_grads, accumulate, sumsq, norm, ws, stream);
+}
+
+int moe_grad_clip(const moe_grad* grads, int64_t n_grads, const double* sumsq, float max_norm,
+                  float* norm, float* coef, void* stream) {
+  const int rc = check_grads(grads, n_grads);
+  if (rc) return rc;
+  if (!sumsq || !(max_norm >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  return launch_grad_clip(grads, n_grads, sumsq, max_norm, norm, coef, stream);
+}
+
+int moe_grad_clip_norm(const moe_grad* grads, int64_t n_grads, float max_norm, double* sumsq,
+                       float* norm, float* coef, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_grads(grads, n_grads);
+  if (rc) return rc;
+  if (!sumsq || !(max_norm >= 0.0f) || !ws || ws_bytes < grad_ws_bytes(n_grads))
+    return MOE_ERR_INVALID_ARG;
+  rc = launch_grad_norm(grads, n_grads, 0, sumsq, nullptr, ws, stream);
+  if (rc) return rc;
+  return launch_grad_clip(grads, n_grads, sumsq, max_norm, norm, coef, stream);
 }
 
 int moe_bias_update(const moe_dims* dims, const int32_t* counts, float gamma,

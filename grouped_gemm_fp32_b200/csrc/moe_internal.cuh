@@ -151,7 +151,8 @@ inline int64_t rows_total(const moe_dims& dm) { return rows_routed(dm) + (int64_
 
 // Launch helpers implemented in the .cu files (all return a moe_status).
 int launch_gate_topk(const moe_dims& dm, const void* x, const float* wg, const float* bias,
-                     int32_t* idx, float* w, float* probs, void* ws, void* stream);
+                     int32_t* idx, float* w, float* probs, float* logits, void* ws,
+                     void* stream);
 int launch_permute(const moe_dims& dm, const int32_t* idx, const void* x, int32_t* counts,
                    int32_t* offsets, int32_t* sorted_ids, int32_t* row_of, void* x_perm, void* ws,
                    void* stream);
@@ -162,6 +163,8 @@ int launch_router_bwd(const moe_dims& dm, const void* x, const float* wg, const 
                       const int32_t* idx, const float* w, const float* dw,
                       const float* seq_grad, int64_t seq_len, float* dlogits, void* dx,
                       float* dwg, int accumulate, void* ws, void* stream);
+int launch_gate_bwd(const moe_dims& dm, const void* x, const float* wg, const float* dlogits,
+                    void* dx, float* dwg, int accumulate, void* ws, void* stream);
 int launch_bias_update(const moe_dims& dm, const int32_t* counts, float gamma,
                        const float* bias_in, float* bias_out, void* stream);
 int launch_seq_balance(const moe_dims& dm, int64_t seq_len, float alpha, const int32_t* idx,
@@ -175,6 +178,34 @@ int launch_combine(const moe_dims& dm, const void* y, const void* y_shared,
                    const int32_t* row_of, const float* w, void* out, bool f32_out, void* stream);
 int launch_combine_bwd(const moe_dims& dm, const void* ws, const void* dout, const void* y,
                        const int32_t* row_of, const float* w, void* dy, float* dw, void* stream);
+
+// Routers of other kinds (route.cu), block norms (norm.cu), gradient norm and clipping
+// (grads.cu); each returns a moe_status.
+int launch_route_topk(const moe_dims& dm, const moe_route_cfg& c, int type, const void* logits,
+                      const float* bias, int32_t* idx, float* w, float* probs, void* stream);
+int launch_route_bwd(const moe_dims& dm, const moe_route_cfg& c, int type, const void* logits,
+                     const int32_t* idx, const float* w, const float* dw, const float* seq_grad,
+                     int64_t seq_len, void* dlogits, void* stream);
+struct NormArgs {  // operands of moe_block_norm[_bwd] (device pointers, include/moe.h)
+  const void *y, *res;  // res: the residual (forward) or u (backward)
+  const float *w_post, *gate, *w_pre;
+  void *u, *n;                  // forward outputs
+  const void *dn, *du;          // backward inputs
+  void *dy, *dres;              // backward outputs
+  float *dw_post, *dgate, *dw_pre;
+  int accumulate;
+  void* ws;
+};
+size_t norm_ws_bytes(const moe_dims& dm, const moe_norm_cfg& c);
+int launch_block_norm(const moe_dims& dm, const moe_norm_cfg& c, int res_type, const NormArgs& a,
+                      void* stream);
+int launch_block_norm_bwd(const moe_dims& dm, const moe_norm_cfg& c, int res_type,
+                          const NormArgs& a, void* stream);
+size_t grad_ws_bytes(int64_t n_grads);
+int launch_grad_norm(const moe_grad* g, int64_t n, int accumulate, double* sumsq, float* norm,
+                     void* ws, void* stream);
+int launch_grad_clip(const moe_grad* g, int64_t n, const double* sumsq, float max_norm,
+                     float* norm, float* coef, void* stream);
 
 enum GemmMode { MODE_FWD1 = 0, MODE_FWD2, MODE_DX2, MODE_DX1, MODE_DW2, MODE_DW1 };
 

@@ -118,6 +118,19 @@ __global__ void __launch_bounds__(DL_WARPS * 32)
   }
 }
 
+// dlogits [T, E] given by the caller -> the same three planes.
+__global__ void split_dlogits_kernel(const float* __restrict__ dlogits, int64_t T, int t_pad,
+                                     int E, int e_pad, __nv_bfloat16* __restrict__ planes) {
+  const int64_t plane = (int64_t)t_pad * e_pad;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < plane;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t t = i / e_pad;
+    const int e = (int)(i - t * e_pad);
+    split3(t < T && e < E ? dlogits[t * E + e] : 0.0f, planes[i], planes[plane + i],
+           planes[2 * plane + i]);
+  }
+}
+
 // dwg[e, c] (+)= sum_s partial[s][e][c], s ascending; four columns per thread.
 __global__ void reduce_dwg_kernel(const float4* __restrict__ partial, int splits, int e_pad,
                                   int E, int d, int accumulate, float4* __restrict__ dwg) {
@@ -265,36 +278,24 @@ int launch_seq_balance(const moe_dims& dm, int64_t seq_len, float alpha, const i
   return cuda_ok(cudaGetLastError()) ? MOE_OK : MOE_ERR_CUDA;
 }
 
-int launch_router_bwd(const moe_dims& dm, const void* x, const float* wg, const float* probs,
-                      const int32_t* idx, const float* w, const float* dw,
-                      const float* seq_grad, int64_t seq_len, float* dlogits, void* dx,
-                      float* dwg, int accumulate, void* ws, void* stream) {
+// No tokens: dX untouched, dWg = 0 (or unchanged).
+static int no_token_dwg(const moe_dims& dm, float* dwg, int accumulate, cudaStream_t st) {
+  if (!accumulate && !cuda_ok(cudaMemsetAsync(dwg, 0, sizeof(float) * (size_t)dm.E * dm.d, st)))
+    return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+// dX += dlogit Wg and dWg (+)= dlogit^T X from the two operands' planes in the workspace.
+static int gate_gemms(const moe_dims& dm, const void* x, void* dx, float* dwg, int accumulate,
+                      void* ws, void* stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const WsLayout L = ws_layout(dm);
   uint8_t* wsb = reinterpret_cast<uint8_t*>(ws);
   int* status = reinterpret_cast<int*>(ws);
-  if (dm.T == 0) {  // no tokens: dX untouched, dWg = 0 (or unchanged)
-    if (!accumulate &&
-        !cuda_ok(cudaMemsetAsync(dwg, 0, sizeof(float) * (size_t)dm.E * dm.d, st)))
-      return MOE_ERR_CUDA;
-    return MOE_OK;
-  }
-  void* wg_planes = wsb + L.gate_split;
-  __nv_bfloat16* dl_planes = reinterpret_cast<__nv_bfloat16*>(wsb + L.dl_planes);
   float* partial = reinterpret_cast<float*>(wsb + L.gdw_part);
-  int rc = launch_split_wg(dm, wg, wg_planes, stream);
+  int rc = launch_gate_dx(dm, wsb + L.dl_planes, wsb + L.gate_split, dx, status, stream);
   if (rc != MOE_OK) return rc;
-  {
-    int64_t blocks = (L.t_pad + DL_WARPS - 1) / DL_WARPS;
-    if (blocks > 8192) blocks = 8192;
-    dlogits_kernel<<<(unsigned)blocks, DL_WARPS * 32, 0, st>>>(
-        probs, idx, w, dw, seq_grad, seq_len, dm.T, L.t_pad, dm.E, L.e_pad, dm.k, dlogits,
-        dl_planes);
-    if (!cuda_ok(cudaGetLastError())) return MOE_ERR_CUDA;
-  }
-  rc = launch_gate_dx(dm, dl_planes, wg_planes, dx, status, stream);
-  if (rc != MOE_OK) return rc;
-  rc = launch_gate_dw(dm, dl_planes, x, partial, status, stream);
+  rc = launch_gate_dw(dm, wsb + L.dl_planes, x, partial, status, stream);
   if (rc != MOE_OK) return rc;
   {
     const int64_t n4 = (int64_t)dm.E * dm.d / 4;
@@ -305,6 +306,47 @@ int launch_router_bwd(const moe_dims& dm, const void* x, const float* wg, const 
         reinterpret_cast<float4*>(dwg));
   }
   return cuda_ok(cudaGetLastError()) ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int launch_router_bwd(const moe_dims& dm, const void* x, const float* wg, const float* probs,
+                      const int32_t* idx, const float* w, const float* dw,
+                      const float* seq_grad, int64_t seq_len, float* dlogits, void* dx,
+                      float* dwg, int accumulate, void* ws, void* stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dm.T == 0) return no_token_dwg(dm, dwg, accumulate, st);
+  const WsLayout L = ws_layout(dm);
+  uint8_t* wsb = reinterpret_cast<uint8_t*>(ws);
+  const int rc = launch_split_wg(dm, wg, wsb + L.gate_split, stream);
+  if (rc != MOE_OK) return rc;
+  {
+    int64_t blocks = (L.t_pad + DL_WARPS - 1) / DL_WARPS;
+    if (blocks > 8192) blocks = 8192;
+    dlogits_kernel<<<(unsigned)blocks, DL_WARPS * 32, 0, st>>>(
+        probs, idx, w, dw, seq_grad, seq_len, dm.T, L.t_pad, dm.E, L.e_pad, dm.k, dlogits,
+        reinterpret_cast<__nv_bfloat16*>(wsb + L.dl_planes));
+    if (!cuda_ok(cudaGetLastError())) return MOE_ERR_CUDA;
+  }
+  return gate_gemms(dm, x, dx, dwg, accumulate, ws, stream);
+}
+
+int launch_gate_bwd(const moe_dims& dm, const void* x, const float* wg, const float* dlogits,
+                    void* dx, float* dwg, int accumulate, void* ws, void* stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dm.T == 0) return no_token_dwg(dm, dwg, accumulate, st);
+  const WsLayout L = ws_layout(dm);
+  uint8_t* wsb = reinterpret_cast<uint8_t*>(ws);
+  const int rc = launch_split_wg(dm, wg, wsb + L.gate_split, stream);
+  if (rc != MOE_OK) return rc;
+  {
+    const int64_t n = (int64_t)L.t_pad * L.e_pad;
+    int64_t blocks = (n + 255) / 256;
+    if (blocks > 8192) blocks = 8192;
+    split_dlogits_kernel<<<(unsigned)blocks, 256, 0, st>>>(
+        dlogits, dm.T, L.t_pad, dm.E, L.e_pad,
+        reinterpret_cast<__nv_bfloat16*>(wsb + L.dl_planes));
+    if (!cuda_ok(cudaGetLastError())) return MOE_ERR_CUDA;
+  }
+  return gate_gemms(dm, x, dx, dwg, accumulate, ws, stream);
 }
 
 int launch_bias_update(const moe_dims& dm, const int32_t* counts, float gamma,

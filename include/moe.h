@@ -18,6 +18,12 @@
  *                                                               moe_router_bwd_seqbal)
  *   aux-loss-free bias step                                    (moe_bias_update)
  *   combine with the shared rows apart (expert parallelism)    (moe_combine_split)
+ *   routers of other kinds: sigmoid scores, expert groups      (moe_gate_logits, moe_route_topk,
+ *                                                               moe_route_bwd, moe_gate_bwd)
+ *   norms around the layer, with gate and residual scale       (moe_block_norm,
+ *                                                               moe_block_norm_bwd)
+ *   global gradient norm and clipping                          (moe_grad_norm, moe_grad_clip,
+ *                                                               moe_grad_clip_norm)
  *
  * Conventions for every call:
  *   - All tensor pointers are DEVICE pointers owned by the caller; the library
@@ -532,6 +538,185 @@ int grouped_gemm_fwd_ep(const moe_dims* dims_loc, const void* ws, const moe_ep_p
 int grouped_gemm_bwd_dx_ep(const moe_dims* dims_loc, const void* ws, const moe_ep_peers* peers,
                            int which, const void* dy_recv, const void* dy_shared, const void* w,
                            const void* a1, void* out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Element types of the calls below that take one. */
+enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 };
+
+/* ---------------------------------------------------------------------------
+ * Routers of other kinds: the choice from given logits, its backward, and the
+ * gate's GEMMs on their own.
+ *
+ * How a router scores and chooses.  Only T, E and k of dims are used by
+ * moe_route_topk and moe_route_bwd: any 1 <= k <= E <= 256. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct moe_route_cfg {
+  int32_t score;      /* MOE_SCORE_SOFTMAX: p = softmax(logits) over the E experts;
+                         MOE_SCORE_SIGMOID: p = 1 / (1 + exp(-logit)), each expert alone */
+  int32_t n_group;    /* groups of E / n_group consecutive experts; 1: no groups */
+  int32_t topk_group; /* groups a token chooses its experts from, <= n_group */
+  int32_t group_top;  /* a group's score is the sum of its group_top (1 or 2) best s */
+  int32_t renorm;     /* 1: the weights are renormalised over the chosen k; 0: w = scale p */
+  float scale;        /* factor of the weights (finite) */
+} moe_route_cfg;
+
+/* The choice of k experts per token from its logits.
+ * Passage: dots.llm1 Technical Report, §Architecture "Mixture of Experts layer"
+ * (top-k of the affinities) and "Load balancing" (the bias only decides the
+ * choice).  The pages route by softmax without groups; sigmoid affinities,
+ * groups and the weights' factor have no counterpart on them.
+ *   s = p + bias;  with n_group > 1 only the experts of the topk_group groups of
+ *   largest group score stay;  topk_idx = the k largest s, descending;
+ *   w[j] = scale p[e_j] / sum_i p[e_i]   (renorm; otherwise scale p[e_j])
+ *   logits   [T, E]  f32 or bf16 (logits_type)
+ *   bias     [E]     f32 (may be NULL: zero)
+ * Out:
+ *   topk_idx [T, k] int32, topk_w [T, k] f32
+ *   probs    [T, E]  f32  affinities that sum to 1 over a token's experts: p for
+ *                    softmax, p / sum_e p for sigmoid (may be NULL)
+ * The choice is the one that 64-bit arithmetic makes on these logits; equal
+ * scores go to the lower expert (equal group scores to the lower group).
+ * Without a bias the experts rank by their logits.  A logit of -inf takes an
+ * expert out (p = 0, s = -inf), a bias of -inf keeps it from being chosen, and a
+ * NaN score ranks as -inf.  A pick that ranks at -inf (fewer than k experts are
+ * left) has weight 0, and so have all picks of a token without any expert; the
+ * picks are k distinct experts in [0, E) in every case.  A NaN or +inf logit
+ * makes the weights NaN where the formulas do. */
+int moe_route_topk(const moe_dims* dims, const moe_route_cfg* cfg, int logits_type,
+                   const void* logits, const float* bias, int32_t* topk_idx, float* topk_w,
+                   float* probs, void* stream);
+
+/* Backward of moe_route_topk: dL/dlogits from the gradient of the weights and,
+ * optionally, of the affinities (Passage: as moe_router_bwd and
+ * moe_router_bwd_seqbal above, whose softmax form without groups this is when
+ * scale = 1).  The choice itself is piecewise constant.  With Z = sum of the
+ * chosen p, D = sum_i dw_i w_i, and C the picks whose weight is not 0:
+ *   dp_j = (scale dw_j - D) / Z  (renorm)  or  scale dw_j       for j in C
+ *   softmax: dp += g;  dlogit_e = p_e (dp_e - sum_i p_i dp_i)
+ *   sigmoid: dp_e += (g_e - sum_i q_i g_i) / sum_i p_i, q the affinities;
+ *            dlogit_e = dp_e p_e (1 - p_e)
+ *   g = seq_grad[t / seq_len] (dL/dprobs, as moe_seq_balance_loss writes it) or 0
+ *   logits   [T, E]  as given to the forward (logits_type)
+ *   topk_idx, topk_w [T, k]  the forward's outputs; dw [T, k] f32
+ *   seq_grad [ceil(T / seq_len), E] f32 (may be NULL: seq_len is not used)
+ * Out: dlogits [T, E] of logits_type.  A topk_idx entry outside [0, E) is
+ * skipped.  The same inputs give the same bits. */
+int moe_route_bwd(const moe_dims* dims, const moe_route_cfg* cfg, int logits_type,
+                  const void* logits, const int32_t* topk_idx, const float* topk_w,
+                  const float* dw, const float* seq_grad, int64_t seq_len, void* dlogits,
+                  void* stream);
+
+/* The gate's logits on their own (Passage: as moe_gate_topk: FP32 gating):
+ * logits [T, E] f32 = x Wg^T, the sums that moe_gate_topk routes by, bit for bit.
+ * x [T, d] bf16, wg [E, d] f32, ws / ws_bytes and requirements as there. */
+int moe_gate_logits(const moe_dims* dims, const void* x, const float* wg, float* logits, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* The gate's gradients from those of its logits (Passage: as moe_router_bwd,
+ * whose two GEMMs these are): dx += dlogits Wg, dwg (+)= dlogits^T x.
+ *   dlogits [T, E] f32; dx [T, d] bf16 read-modify-write; dwg [E, d] f32 written,
+ *   or added to when accumulate != 0; ws / ws_bytes and requirements as there. */
+int moe_gate_bwd(const moe_dims* dims, const void* x, const float* wg, const float* dlogits,
+                 void* dx, float* dwg, int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The norms before and after a block, with the block's gate and the residual's
+ * scale.  A block (the MoE layer, attention) reads a normed copy n of the
+ * residual stream and its output y joins the stream. */
+typedef struct moe_norm_cfg {
+  float eps;         /* added to the mean square under the root, > 0 */
+  float res_scale;   /* alpha, factor of the residual */
+  float block_scale; /* beta, factor of the block's output */
+  int64_t seq_len;   /* tokens that share a row of the gate; 0: one row for all */
+} moe_norm_cfg;
+
+/* One block boundary in one pass (no counterpart on the pages, which only norm
+ * queries and keys):
+ *   z = y / sqrt(mean(y^2) + eps) * w_post     (w_post NULL: z = y)
+ *   u = alpha res + beta gate[t / seq_len] * z (gate NULL: 1)
+ *   n = u / sqrt(mean(u^2) + eps) * w_pre
+ *   res_type     MOE_BF16 or MOE_F32, type of the residual stream and its gradients
+ *   y     [T, d] bf16, the block's output.  NULL: no block yet, u = res; then w_post,
+ *                gate and res_out must be NULL too
+ *   res   [T, d] res_type
+ *   w_post, w_pre [d] f32; gate [max(1, ceil(T / seq_len)), d] f32 (one row where
+ *                seq_len = 0)
+ * Out:
+ *   res_out [T, d] res_type = u (may be res itself)
+ *   n     [T, d] bf16, the next block's input; NULL with w_pre NULL: no pre-norm
+ * n is computed from u before u is rounded to res_type.  FP32 throughout: rows of
+ * |values| below 1e18.  Requires d <= 16384 and 16-byte aligned tensors. */
+int moe_block_norm(const moe_dims* dims, const moe_norm_cfg* cfg, int res_type, const void* y,
+                   const void* res, const float* w_post, const float* gate, const float* w_pre,
+                   void* res_out, void* n, void* stream);
+
+/* Workspace of moe_block_norm_bwd in bytes (host-side, no counterpart on the
+ * pages); 0 for invalid dims or cfg. */
+size_t moe_norm_workspace_size(const moe_dims* dims, const moe_norm_cfg* cfg);
+
+/* Backward of moe_block_norm (no counterpart on the pages), from the saved y and
+ * u = res_out (as stored):
+ *   du  = dres_out + gradient of the pre-norm at u applied to dn
+ *   dres = alpha du;   dy = gradient of the post-norm at y applied to beta gate * du
+ *   dw_pre = sum_t dn * u / rms(u);   dw_post = sum_t beta gate * du * y / rms(y)
+ *   dgate[s] = sum over the tokens t of row s of beta du * z
+ *   dn    [T, d] bf16, gradient of n (NULL: no pre-norm; then w_pre and dw_pre NULL)
+ *   dres_out [T, d] res_type, gradient of res_out (NULL: zero); not both NULL
+ *   y     [T, d] bf16 (NULL: no block; then w_post, gate, dy, dw_post, dgate NULL and
+ *         dres = du)
+ *   u     [T, d] res_type, the forward's res_out (res itself when y was NULL); may be
+ *         NULL when dn is
+ * Out:
+ *   dy    [T, d] bf16; dres [T, d] res_type (may be dres_out itself)
+ *   dw_post, dw_pre [d] f32, dgate as gate, f32: written, or added to when
+ *         accumulate != 0; each may be NULL (not wanted)
+ * Sums over tokens run in a fixed order: the same inputs give the same bits.
+ * Two calls on one workspace must not overlap on the GPU. */
+int moe_block_norm_bwd(const moe_dims* dims, const moe_norm_cfg* cfg, int res_type,
+                       const void* dn, const void* dres_out, const void* y, const void* u,
+                       const float* w_post, const float* gate, const float* w_pre, void* dy,
+                       void* dres, float* dw_post, float* dgate, float* dw_pre, int accumulate,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The global norm of many gradient tensors, and their clipping.
+ * Passage: dots.llm1 Technical Report, §Training (AdamW with gradients clipped to
+ * a norm of 1.0).  A list is an array in HOST memory, read before the call
+ * returns; its tensors are device memory of any element-aligned address. */
+typedef struct moe_grad {
+  const void* data; /* n elements (may be NULL when n = 0) */
+  void* out;        /* where the clipped elements go; NULL or data: in place.  Otherwise
+                       it must not overlap any tensor of the list */
+  int64_t n;
+  int32_t type;     /* MOE_F32, MOE_BF16 or MOE_F16, of data and out */
+} moe_grad;
+
+/* Bytes of device workspace for lists of up to n_grads tensors (host-side, no
+ * counterpart on the pages). */
+size_t moe_grad_workspace_size(int64_t n_grads);
+
+/* Sum of the squares of every element of the list (Passage: as above).
+ *   sumsq [1] f64 (device): written, or added to when accumulate != 0
+ *   norm  [1] f32 (device, may be NULL): sqrt(sumsq)
+ * Sharded gradients: add the ranks' sumsq, then moe_grad_clip.  Elements are
+ * squared and added without overflow or loss of small ones (64-bit sums), in an
+ * order fixed by the list's sizes: the same list of values gives the same bits.
+ * Two calls on one workspace must not overlap on the GPU. */
+int moe_grad_norm(const moe_grad* grads, int64_t n_grads, int accumulate, double* sumsq,
+                  float* norm, void* ws, size_t ws_bytes, void* stream);
+
+/* Clipping by a given sum of squares (Passage: as above):
+ *   coef = min(1, max_norm / (sqrt(sumsq) + 1e-6));  out = coef * data
+ * rounded once to the tensor's type.  norm [1] f32 = sqrt(sumsq) and coef [1] f32
+ * (device, each may be NULL) are written.  Tensors clipped in place are left
+ * alone when coef = 1.  A sumsq that is not finite gives the formula's coef: 0 for
+ * an infinite norm, NaN for a NaN.  max_norm >= 0 (infinity: never clips). */
+int moe_grad_clip(const moe_grad* grads, int64_t n_grads, const double* sumsq, float max_norm,
+                  float* norm, float* coef, void* stream);
+
+/* moe_grad_norm (accumulate = 0), then moe_grad_clip (Passage: as above). */
+int moe_grad_clip_norm(const moe_grad* grads, int64_t n_grads, float max_norm, double* sumsq,
+                       float* norm, float* coef, void* ws, size_t ws_bytes, void* stream);
 
 /* Reads and clears the device status word of `ws` (synchronises `stream`).
  * Error reporting of this library: the pages have no counterpart.

@@ -1,0 +1,290 @@
+"""moe_route_topk and moe_route_bwd against their 64-bit forms, and the layer's gate
+GEMMs on their own (moe_gate_logits, moe_gate_bwd).
+
+The choice has to be the 64-bit one exactly.  Bounds of FP32 results count roundings:
+an affinity takes the rounding of x - max (|x - max| 2^-24), expf (2 steps of 2^-23), a
+sum of up to 256 terms (at most 14 roundings on any path, twice for the chosen ones'
+sum), a reciprocal and three products: (24 + |x - max|) 2^-23 of its value covers them
+for p and for w."""
+import itertools
+import math
+
+import pytest
+import torch
+
+import grouped_gemm_fp32_b200 as moe
+import ref64
+from common import dev
+import synth
+
+pytestmark = pytest.mark.gpu
+SM, SG = "softmax", "sigmoid"
+INF = math.inf
+
+
+def make(T, E, k, seed=0, bias=True, dtype=torch.float32, std=1.28, **cfg):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    cfg = dict(score=SM, n_group=1, topk_group=1, group_top=2, renorm=True, scale=1.0, k=k) | cfg
+    x = (std * torch.randn(T, E, generator=g, device="cuda")).to(dtype)
+    b = 0.05 * (torch.rand(E, generator=g, device="cuda") - 0.5) if bias else None
+    return x, b, cfg
+
+
+def call(x, b, cfg, probs=True, stream=None):
+    T, E = x.shape
+    k = cfg["k"]
+    dm = moe.MoeDims.of(T, 64, E, k, 0, 64, 64)
+    rc = moe.MoeRouteCfg.of(*[cfg[n] for n in ("score", "n_group", "topk_group", "group_top",
+                                               "renorm", "scale")])
+    idx = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), 7.0, device="cuda")
+    p = torch.full((T, E), 7.0, device="cuda") if probs else None
+    moe.moe_route_topk(dm, rc, x, b, idx, w, p, stream)
+    return dm, rc, idx, w, p
+
+
+def spread(x):
+    x = x.double().masked_fill(~x.isfinite(), 0.0)
+    return (x - x.amax(1, keepdim=True)).abs()
+
+
+def check(x, b, cfg):
+    dm, rc, idx, w, p = call(x, b, cfg)
+    ridx, rw, rp, raw = ref64.route(x, b, cfg)
+    assert torch.equal(idx, ridx), (idx != ridx).nonzero()[:5]
+    # sigmoid: no maximum is subtracted, and p / sum p is what stands in w and probs
+    far = spread(x) if cfg["score"] == SM else torch.zeros_like(x, dtype=torch.float64)
+    rel = (24 + far) * 2 ** -23
+    ref64.within(p, rp, rel * rp.nan_to_num() + 2.0 ** -126, "probs")
+    wrel = rel.gather(1, ridx.long()).amax(1, keepdim=True) * 2
+    ref64.within(w, rw, wrel * rw.nan_to_num() + 2.0 ** -126, "weights")
+    return dm, rc, idx, w, p
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("T,E,k", [(1, 128, 6), (3, 8, 2), (5, 1, 1), (130, 7, 7), (257, 33, 5),
+                                   (64, 64, 8), (1000, 96, 6), (77, 256, 8), (31, 250, 40),
+                                   (2, 256, 256), (4099, 128, 6)])
+def test_topk_matches_64_bits(T, E, k, score):
+    for dtype, bias in itertools.product((torch.float32, torch.bfloat16), (True, False)):
+        check(*make(T, E, k, T + E, bias, dtype, score=score, scale=2.5))
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("E,G,K,top,k", [(256, 8, 4, 2, 8), (256, 8, 4, 1, 8), (128, 4, 1, 2, 6),
+                                         (160, 8, 3, 2, 6), (96, 3, 2, 2, 5), (60, 5, 2, 1, 4),
+                                         (256, 64, 7, 2, 9), (256, 256, 9, 1, 9),
+                                         (48, 16, 16, 2, 3), (250, 2, 1, 2, 100)])
+def test_groups_match_64_bits(E, G, K, top, k, score):
+    for dtype, bias in itertools.product((torch.float32, torch.bfloat16), (True, False)):
+        check(*make(515, E, k, E + G, bias, dtype, score=score, n_group=G, topk_group=K,
+                    group_top=top, scale=1.5))
+
+
+def test_without_renormalisation():
+    check(*make(200, 128, 6, 1, renorm=False, scale=0.5))
+    check(*make(200, 128, 6, 1, renorm=False, score=SG))
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+def test_near_and_equal_scores(score):
+    # scores a few steps of FP32 apart or equal, so that FP32 alone could not order them
+    T, E = 512, 128
+    g = torch.Generator(device="cuda").manual_seed(5)
+    base = torch.randint(0, 4, (T, E), generator=g, device="cuda").float()
+    x = base + 2.0 ** -22 * torch.randint(0, 4, (T, E), generator=g, device="cuda")
+    b = 2.0 ** -26 * torch.randint(0, 8, (E,), generator=g, device="cuda").float()
+    for groups in (dict(), dict(n_group=8, topk_group=3)):
+        cfg = dict(score=score, n_group=1, topk_group=1, group_top=2, renorm=True, scale=1.0,
+                   k=6) | groups
+        check(x, b, cfg)
+        check(x, None, cfg)
+        check(base, torch.zeros_like(b), cfg)
+        check(torch.zeros_like(x), None, cfg)       # every score equal: the first k
+        check(torch.full_like(x, -3.0), b * 0, cfg)
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("groups", [dict(), dict(n_group=4, topk_group=2)])
+def test_masked_experts(score, groups):
+    x, b, cfg = make(64, 32, 6, 3, score=score, **groups)
+    x[0] = -INF                  # a token without any expert
+    x[1, 3:] = -INF              # three left for six picks
+    x[2, :31] = -INF
+    x[3, ::2] = -INF
+    x[4, 8:16] = -INF
+    check(x, b, cfg)
+    check(x, None, cfg)
+    b2 = b.clone()
+    b2[5:30] = -INF              # experts that the bias keeps out
+    _, _, idx, w, _ = check(x, b2, cfg)
+    assert (w[0] == 0).all()
+    assert all(len(set(r)) == 6 for r in idx.tolist())
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+def test_lowest_values_and_wide_ranges(score):
+    # the lowest value of the type in masked places is an ordinary, very small logit
+    low = torch.finfo(torch.float32).min
+    x, b, cfg = make(16, 64, 4, 4, score=score)
+    x[:, ::3] = low
+    x[1] = low
+    check(x, b, cfg)
+    x, b, cfg = make(64, 64, 4, 4, score=score, std=30.0)
+    check(x, b, cfg)
+    x = x - 200.0                # every sigmoid below FP32's normal range
+    if score == SG:
+        _, _, idx, w, _ = call(x, None, cfg)
+        ridx, rw, _, _ = ref64.route(x, None, cfg)
+        assert torch.equal(idx, ridx)
+        ref64.within(w, rw, 1e-5 * rw + 2.0 ** -126, "weights of tiny affinities")
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+def test_non_finite_logits_keep_the_choice_valid(score):
+    x, b, cfg = make(40, 64, 6, 6, score=score)
+    x[0, 5] = math.nan
+    x[1] = math.nan
+    x[2, 9] = INF
+    x[3, 4] = math.nan
+    x[3, 10:] = -INF
+    for bias in (b, None):
+        _, _, idx, w, p = call(x, bias, cfg)
+        assert all(len(set(r)) == 6 and 0 <= min(r) and max(r) < 64 for r in idx.tolist())
+        assert w[4:].isfinite().all() and p[4:].isfinite().all()   # other tokens unharmed
+        ridx, rw, rp, _ = ref64.route(x, bias, cfg)
+        assert torch.equal(idx, ridx)
+        assert torch.equal(w.isnan(), rw.isnan()) and torch.equal(p.isnan(), rp.isnan())
+
+
+def bwd_check(x, idx, w, dw, cfg, rc, dm, seq_grad=None, seq_len=0):
+    dl = torch.full_like(x, 9.0)
+    moe.moe_route_bwd(dm, rc, x, idx, w, dw, seq_grad, seq_len, dl)
+    ref, mag = ref64.route_bwd(x, idx, w, dw, cfg, seq_grad, seq_len)
+    # twice an affinity's bound (p and the chosen sum), and the sums over k picks and E experts
+    far = spread(x).where(x != -INF, 0.0) if cfg["score"] == SM \
+        else torch.zeros_like(x, dtype=torch.float64)
+    rel = (64 + cfg["k"] + 2 * far.amax(1, keepdim=True)) * 2 ** -23
+    ref64.within(dl, ref, rel * mag + ref64.HALF[x.dtype] * ref.abs() + 2.0 ** -126, "dlogits")
+    again = torch.full_like(x, 9.0)
+    moe.moe_route_bwd(dm, rc, x, idx, w, dw, seq_grad, seq_len, again)
+    assert torch.equal(dl, again)
+    return dl
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("T,E,k,groups,seq_len", [(1, 128, 6, {}, 0), (5, 1, 1, {}, 0),
+                                                  (300, 8, 2, {}, 128), (257, 33, 5, {}, 7),
+                                                  (515, 256, 8, dict(n_group=8, topk_group=4), 0),
+                                                  (2000, 128, 6, {}, 1500), (9, 256, 256, {}, 4),
+                                                  (130, 250, 40, {}, 0)])
+def test_bwd_matches_64_bits(T, E, k, groups, seq_len, score):
+    for dtype, renorm in itertools.product((torch.float32, torch.bfloat16), (True, False)):
+        x, b, cfg = make(T, E, k, T * E, True, dtype, score=score, scale=2.5, renorm=renorm,
+                         **groups)
+        dm, rc, idx, w, _ = call(x, b, cfg)
+        g = torch.Generator(device="cuda").manual_seed(T)
+        dw = torch.randn(T, k, generator=g, device="cuda")
+        sg = torch.randn(-(-T // seq_len), E, generator=g, device="cuda") if seq_len else None
+        bwd_check(x, idx, w, dw, cfg, rc, dm, sg, seq_len)
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+def test_bwd_is_the_gradient(score):
+    # against central differences of the 64-bit forward with the choice held
+    x, b, cfg = make(6, 24, 4, 8, score=score, scale=1.5)
+    dm, rc, idx, w, _ = call(x, b, cfg)
+    dw = torch.randn(6, 4, device="cuda")
+    sg = torch.randn(2, 24, device="cuda")
+    dl = bwd_check(x, idx, w, dw, cfg, rc, dm, sg, 4)
+
+    def loss(z):
+        p, q = ref64.affinities(z, score)
+        c = p.gather(1, idx.long())
+        w = 1.5 * c / c.sum(1, keepdim=True)
+        return ((w * dw).sum() + (q * sg.double()[torch.arange(6, device="cuda") // 4]).sum())
+
+    h, z = 1e-5, x.double()
+    for t, e in ((0, int(idx[0, 0])), (1, 5), (3, 23), (5, int(idx[5, 3])), (4, 0)):
+        up, dn = z.clone(), z.clone()
+        up[t, e] += h
+        dn[t, e] -= h
+        assert abs(float((loss(up) - loss(dn)) / (2 * h)) - float(dl[t, e])) < 1e-5
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+def test_bwd_of_masked_tokens_and_foreign_indices(score):
+    x, b, cfg = make(40, 32, 6, 3, score=score)
+    x[0] = -INF
+    x[1, 3:] = -INF
+    dm, rc, idx, w, _ = call(x, b, cfg)
+    dw = torch.randn(40, 6, device="cuda")
+    dl = bwd_check(x, idx, w, dw, cfg, rc, dm, torch.randn(1, 32, device="cuda"), 64)
+    assert (dl[x == -INF] == 0).all()
+    idx = idx.clone()
+    idx[3, 1], idx[4, 0], idx[5, 2] = -1, 32, 1 << 30      # no expert: skipped
+    idx[6, 1] = idx[6, 0]                                  # the same expert twice
+    bwd_check(x, idx, w, dw, cfg, rc, dm)
+
+
+def test_no_tokens_and_other_streams_and_graphs():
+    x, b, cfg = make(0, 64, 4)
+    call(x, b, cfg)
+    x, b, cfg = make(700, 256, 8, score=SG, n_group=8, topk_group=4)
+    _, _, idx, w, p = call(x, b, cfg)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        dm, rc, idx2, w2, p2 = call(x, b, cfg, stream=s)
+        dw = torch.randn(700, 8, device="cuda")
+        dl = torch.empty_like(x)
+        moe.moe_route_bwd(dm, rc, x, idx2, w2, dw, None, 0, dl)
+    s.synchronize()
+    assert torch.equal(idx, idx2) and torch.equal(w, w2) and torch.equal(p, p2)
+    ref = dl.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_route_topk(dm, rc, x, b, idx2, w2, p2)
+        moe.moe_route_bwd(dm, rc, x, idx2, w2, dw, None, 0, dl)
+    for t in (idx2, w2, p2, dl):
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(idx, idx2) and torch.equal(w, w2) and torch.equal(dl, ref)
+
+
+@pytest.mark.parametrize("T,d,E,k", [(300, 128, 8, 2), (1000, 192, 96, 6), (129, 256, 256, 8)])
+def test_gate_logits_and_bwd(T, d, E, k):
+    x = dev(synth.normal_bf16(T, 1, (T, d), 1.0), True)
+    wg = dev(synth.normal_f32(T, 2, (E, d), 0.05))
+    dm = moe.MoeDims.of(T, d, E, k, 0, 64, 64)
+    ws = torch.zeros(moe.moe_workspace_size(dm), dtype=torch.uint8, device="cuda")
+    logits = torch.full((T, E), 7.0, device="cuda")
+    moe.moe_gate_logits(dm, x, wg, logits, ws)
+    ref = x.double() @ wg.double().T
+    mag = x.double().abs() @ wg.double().abs().T
+    # products exact; d / 64 blocks of 64 products in the tensor cores' FP32 (truncating:
+    # a whole step of 2^-23 each) and the blocks' sums
+    ref64.within(logits, ref, (64 + d // 64 + 2) * 2.0 ** -23 * mag, "logits")
+    # the library's own softmax router on these logits: moe_gate_topk's choice and weights
+    bias = 0.02 * (torch.rand(E, device="cuda") - 0.5)
+    idx, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    moe.moe_gate_topk(dm, x, wg, bias, idx, w, None, ws)
+    cfg = dict(score=SM, n_group=1, topk_group=1, group_top=2, renorm=True, scale=1.0, k=k)
+    _, _, idx2, w2, _ = call(logits, bias, cfg)
+    same = (idx == idx2).all(1)
+    assert same.float().mean() > 0.99
+    ref64.within(w[same], w2[same], 1e-5, "weights")
+    # backward
+    dl = torch.randn(T, E, device="cuda")
+    dx = torch.randn(T, d, device="cuda").bfloat16()
+    dx0, dwg = dx.clone(), torch.full((E, d), 3.0, device="cuda")
+    for acc in (0, 1):
+        before = dwg.clone()
+        moe.moe_gate_bwd(dm, x, wg, dl, dx if acc == 0 else dx.clone(), dwg, acc, ws)
+        rw = dl.double().T @ x.double() + (before.double() if acc else 0)
+        scale = (dl.double().abs().T @ x.double().abs()).amax()
+        ref64.within(dwg, rw, 1e-4 * scale, "dwg")
+    rx = dx0.double() + dl.double() @ wg.double()
+    ref64.within(dx, rx, 1e-2 * rx.abs().amax(), "dx")
+    assert moe.moe_get_device_status(ws) == 0

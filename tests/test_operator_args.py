@@ -1,0 +1,197 @@
+"""Argument and shape checks of the routers of other kinds, the block norms and the
+gradient norm and clipping: refused before anything is launched (CPU only), by the C
+calls with a status and by the binding with a ValueError that names the tensor."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import grouped_gemm_fp32_b200 as moe
+from grouped_gemm_fp32_b200 import _lib
+
+P = ctypes.c_void_p(4096)       # an address that is never followed: checks come first
+ODD = ctypes.c_void_p(4097)
+OFF8 = ctypes.c_void_p(4104)    # not 16-byte aligned
+NUL = None
+BIG = 1 << 40
+INVALID, SHAPE = -1, -2
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from grouped_gemm_fp32_b200 import build
+    build.build()
+
+
+def dims(T=64, d=128, E=8, k=2):
+    return ctypes.byref(moe.MoeDims.of(T, d, E, k, 0, 64, 64))
+
+
+def route(dm=None, cfg=None, kind=moe.MOE_F32, x=P, idx=P, w=P):
+    cfg = moe.MoeRouteCfg.of() if cfg is None else cfg
+    return moe.load().moe_route_topk(dims() if dm is None else dm, ctypes.byref(cfg), kind, x,
+                                     NUL, idx, w, NUL, NUL)
+
+
+def route_bwd(dm=None, cfg=None, kind=moe.MOE_F32, x=P, idx=P, w=P, dw=P, sg=NUL, L=0, out=P):
+    cfg = moe.MoeRouteCfg.of() if cfg is None else cfg
+    return moe.load().moe_route_bwd(dims() if dm is None else dm, ctypes.byref(cfg), kind, x, idx,
+                                    w, dw, sg, L, out, NUL)
+
+
+def test_route_refusals():
+    R = moe.MoeRouteCfg.of
+    for f in (route, route_bwd):
+        for cfg, status in ((R(score=2), INVALID), (R(n_group=0), INVALID),
+                            (R(n_group=4, topk_group=5), INVALID),
+                            (R(n_group=4, topk_group=0), INVALID), (R(group_top=3), INVALID),
+                            (R(scale=math.nan), INVALID), (R(scale=math.inf), INVALID),
+                            (R(n_group=3, topk_group=1), SHAPE),    # 8 experts in 3 groups
+                            (R(n_group=8, topk_group=3, group_top=2), SHAPE),  # groups of one
+                            (R(n_group=8, topk_group=1, group_top=1), SHAPE)):  # k = 2 of 1
+            assert f(cfg=cfg) == status, (f, cfg.score, cfg.n_group)
+        bad = R()
+        bad.renorm = 2
+        assert f(cfg=bad) == INVALID
+        for dm, status in ((dims(T=-1), INVALID), (dims(E=0), INVALID), (dims(k=0), INVALID),
+                           (dims(E=257), SHAPE), (dims(k=9), SHAPE),
+                           (dims(T=1 << 31, k=1), SHAPE), (NUL, INVALID)):
+            lib = moe.load()
+            cfg = ctypes.byref(R())
+            got = lib.moe_route_topk(dm, cfg, 0, P, NUL, P, P, NUL, NUL) if f is route else \
+                lib.moe_route_bwd(dm, cfg, 0, P, P, P, P, NUL, 0, P, NUL)
+            assert got == status
+        for kind in (moe.MOE_F16, -1, 7):
+            assert f(kind=kind) == INVALID
+        for name in ("x", "idx", "w"):
+            assert f(**{name: NUL}) == INVALID
+    assert route_bwd(dw=NUL) == INVALID and route_bwd(out=NUL) == INVALID
+    assert route_bwd(sg=P, L=0) == INVALID
+    assert moe.load().moe_route_topk(dims(), None, 0, P, NUL, P, P, NUL, NUL) == INVALID
+    # no tokens: nothing is needed, nothing is launched
+    assert route(dm=dims(T=0), x=NUL, idx=NUL, w=NUL) == 0
+    assert route_bwd(dm=dims(T=0), x=NUL, idx=NUL, w=NUL, dw=NUL, out=NUL) == 0
+
+
+def test_gate_refusals():
+    L = moe.load()
+    for dm, status in ((dims(d=100), SHAPE), (dims(E=12), SHAPE), (dims(T=-1), INVALID)):
+        assert L.moe_gate_logits(dm, P, P, P, P, BIG, NUL) == status
+        assert L.moe_gate_bwd(dm, P, P, P, P, P, 0, P, BIG, NUL) == status
+    for i in range(4):
+        a = [P] * 4
+        a[i] = NUL
+        assert L.moe_gate_logits(dims(), *a, BIG, NUL) == INVALID
+    assert L.moe_gate_logits(dims(), P, P, P, P, 8, NUL) == INVALID
+    for i in range(5):
+        a = [P] * 5
+        a[i] = NUL
+        assert L.moe_gate_bwd(dims(), *a, 0, P, BIG, NUL) == INVALID
+    assert L.moe_gate_bwd(dims(), P, P, P, P, P, 0, P, 8, NUL) == INVALID
+
+
+def norm(dm=None, cfg=None, kind=moe.MOE_BF16, y=P, res=P, wp=P, g=P, w=P, out=P, n=P):
+    cfg = moe.MoeNormCfg.of() if cfg is None else cfg
+    return moe.load().moe_block_norm(dims() if dm is None else dm, ctypes.byref(cfg), kind, y, res,
+                                     wp, g, w, out, n, NUL)
+
+
+def norm_bwd(dm=None, cfg=None, kind=moe.MOE_BF16, dn=P, du=P, y=P, u=P, wp=P, g=P, w=P, dy=P,
+             dres=P, dwp=P, dg=P, dw=P, acc=0, ws=P, nbytes=BIG):
+    cfg = moe.MoeNormCfg.of() if cfg is None else cfg
+    return moe.load().moe_block_norm_bwd(dims() if dm is None else dm, ctypes.byref(cfg), kind, dn,
+                                         du, y, u, wp, g, w, dy, dres, dwp, dg, dw, acc, ws,
+                                         nbytes, NUL)
+
+
+def test_norm_refusals():
+    C = moe.MoeNormCfg.of
+    for f in (norm, norm_bwd):
+        for cfg in (C(eps=0.0), C(eps=-1.0), C(eps=math.nan), C(eps=math.inf),
+                    C(res_scale=math.nan), C(block_scale=math.inf), C(seq_len=-1)):
+            assert f(cfg=cfg) == INVALID
+        for dm, status in ((dims(d=96), SHAPE), (dims(d=16448), SHAPE), (dims(T=-1), INVALID),
+                           (dims(T=1 << 31), SHAPE), (dims(d=0), INVALID)):
+            assert f(dm=dm) == status
+        for kind in (moe.MOE_F16, -1, 9):
+            assert f(kind=kind) == INVALID
+    for name in ("y", "res", "wp", "g", "w", "out", "n"):
+        assert norm(**{name: OFF8}) == INVALID, name
+    for name in ("dn", "du", "y", "u", "wp", "g", "w", "dy", "dres", "dwp", "dg", "dw", "ws"):
+        assert norm_bwd(**{name: OFF8}) == INVALID, name
+    # what belongs together
+    assert norm(res=NUL) == INVALID and norm(out=NUL) == INVALID
+    assert norm(w=NUL) == INVALID and norm(n=NUL) == INVALID
+    assert norm(y=NUL) == INVALID                          # a post-norm without a block
+    assert norm(y=NUL, wp=NUL, g=NUL) == INVALID           # res_out without a block
+    assert norm(y=NUL, wp=NUL, g=NUL, out=NUL, w=NUL, n=NUL) == INVALID  # nothing to do
+    assert norm_bwd(dn=NUL) == INVALID                     # w_pre without dn
+    assert norm_bwd(dn=NUL, w=NUL, dw=NUL, du=NUL) == INVALID
+    assert norm_bwd(u=NUL) == INVALID and norm_bwd(w=NUL) == INVALID
+    assert norm_bwd(y=NUL) == INVALID and norm_bwd(dy=NUL) == INVALID
+    assert norm_bwd(wp=NUL) == INVALID and norm_bwd(g=NUL) == INVALID   # their gradients asked
+    assert norm_bwd(dres=NUL) == INVALID and norm_bwd(ws=NUL) == INVALID
+    assert norm_bwd(acc=2) == INVALID
+    need = moe.moe_norm_workspace_size(moe.MoeDims.of(64, 128, 8, 2, 0, 64, 64), C())
+    assert need > 0 and norm_bwd(nbytes=need - 1) == INVALID
+    assert moe.moe_norm_workspace_size(moe.MoeDims.of(64, 96, 8, 2, 0, 64, 64), C()) == 0
+    # one gate row per sequence: the workspace grows with them
+    few, many = (moe.moe_norm_workspace_size(moe.MoeDims.of(4096, 128, 8, 2, 0, 64, 64),
+                                             C(seq_len=s)) for s in (0, 1))
+    assert many > few
+    assert norm(dm=dims(T=0)) == 0
+
+
+def test_grad_refusals():
+    L = moe.load()
+    one = lambda **kw: (moe.MoeGrad * 1)(moe.MoeGrad(**(dict(data=4096, out=None, n=4, type=0) | kw)))  # noqa: E731,E501
+    clip = lambda a, n=1, s=P, m=1.0: L.moe_grad_clip(a, n, s, ctypes.c_float(m), NUL, NUL, NUL)  # noqa: E731,E501
+    for bad in (one(type=3), one(type=-1), one(n=-1), one(data=None), one(data=4097),
+                one(data=4098), one(out=4098), one(out=4097, type=moe.MOE_BF16)):
+        assert clip(bad) == INVALID
+        assert L.moe_grad_norm(bad, 1, 0, P, NUL, P, BIG, NUL) == INVALID
+        assert L.moe_grad_clip_norm(bad, 1, ctypes.c_float(1.0), P, NUL, NUL, P, BIG, NUL) == INVALID
+    ok = one()
+    assert clip(ok, -1) == INVALID and clip(None) == INVALID and clip(ok, s=NUL) == INVALID
+    for m in (-1.0, math.nan):
+        assert clip(ok, m=m) == INVALID
+        assert L.moe_grad_clip_norm(ok, 1, ctypes.c_float(m), P, NUL, NUL, P, BIG, NUL) == INVALID
+    need = moe.moe_grad_workspace_size(1)
+    for args in ((NUL, NUL, P, BIG), (P, NUL, NUL, BIG), (P, NUL, P, need - 1)):
+        assert L.moe_grad_norm(ok, 1, 0, *args, NUL) == INVALID
+        assert L.moe_grad_clip_norm(ok, 1, ctypes.c_float(1.0), args[0], NUL, NUL, args[2],
+                                    args[3], NUL) == INVALID
+    assert L.moe_grad_norm(ok, 1, 2, P, NUL, P, BIG, NUL) == INVALID
+    assert moe.moe_grad_workspace_size(-1) == 0
+    assert moe.moe_grad_workspace_size(100_000) > moe.moe_grad_workspace_size(1) > 0
+
+
+def test_binding_refuses_what_it_cannot_pass(monkeypatch):
+    _lib._types()
+    monkeypatch.setitem(_lib._TYPES, "device", lambda: 0)   # no GPU here: pretend one is current
+    dm, cfg = moe.MoeDims.of(4, 128, 8, 2, 0, 64, 64), moe.MoeRouteCfg.of()
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="logits.*element type"):
+        moe.moe_route_topk(dm, cfg, x.half(), None, 16, 16, None, 0)
+    with pytest.raises(ValueError, match="logits: on cpu"):
+        moe.moe_route_topk(dm, cfg, x, None, 16, 16, None, 0)
+    with pytest.raises(ValueError, match="logits: shape"):
+        moe.moe_route_topk(dm, cfg, x[:3], None, 16, 16, None, 0)
+    with pytest.raises(ValueError, match="logits: not contiguous"):
+        moe.moe_route_topk(dm, cfg, torch.zeros(8, 4).T, None, 16, 16, None, 0)
+    n = moe.MoeNormCfg.of()
+    with pytest.raises(ValueError, match="y: torch.float32"):
+        moe.moe_block_norm(dm, n, torch.zeros(4, 128), torch.zeros(4, 128), None, None, None, 16,
+                           None, 0)
+    with pytest.raises(ValueError, match="res: unsupported"):
+        moe.moe_block_norm(dm, n, None, torch.zeros(4, 128, dtype=torch.int32), None, None, 16,
+                           None, 16, 0)
+    with pytest.raises(ValueError, match="gradient: on cpu"):
+        moe.GradList([torch.zeros(4)])
+    with pytest.raises(ValueError, match="gradient: not contiguous"):
+        moe.GradList([torch.zeros(4, 4).T])
+    with pytest.raises(ValueError, match="unsupported element type"):
+        moe.GradList([torch.zeros(4, dtype=torch.float64)])
+    with pytest.raises(ValueError, match="2 gradients, 1 outs"):
+        moe.GradList([1, 2], [3])
