@@ -5,9 +5,9 @@
 // writes it once.  The list travels as a kernel argument (up to GL_MAX tensors a
 // launch), so nothing is copied to the device and a captured graph holds its own.
 //
-// A launch splits its tensors into chunks of GL_CHUNK elements of one tensor each;
-// CTA b takes chunks b, b + gridDim, ... .  Squares are exact in 64 bits (an FP32
-// value's square has 48 significant bits) and are added in 64 bits: no overflow,
+// A launch splits its tensors into chunks of up to GL_CHUNK elements of one tensor
+// each; CTA b takes chunks b, b + gridDim, ... .  Squares are exact in 64 bits (an
+// FP32 value's square has 48 significant bits) and are added in 64 bits: no overflow,
 // no lost small elements.  Every sum runs in an order fixed by the list's sizes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -19,9 +19,10 @@ namespace moe {
 namespace {
 
 constexpr int GL_MAX = 512;      // tensors per launch
-constexpr int GL_CTAS = 592;     // CTAs of a norm launch: one partial sum each
+constexpr int GL_CTAS = 592;     // CTAs of a launch (four an SM); a norm launch's partial sums
 constexpr int GL_THREADS = 256;
-constexpr int GL_CHUNK = 16384;  // elements
+constexpr int GL_CHUNK = 16384;  // most elements of a chunk: 8 vectors a thread of bf16
+constexpr int GL_CHUNK_MIN = 2048;
 
 struct GradEnt {
   const void* data;
@@ -34,6 +35,7 @@ struct GradTable {
   GradEnt e[GL_MAX];
   uint8_t type[GL_MAX];
   int n;
+  int chunk;       // elements of a chunk: less than GL_CHUNK where that fills more CTAs
   int64_t chunks;
 };
 
@@ -55,15 +57,67 @@ __device__ __forceinline__ int find(const GradTable& tb, int64_t chunk) {
   return lo;
 }
 
+// The part [v0, v1) of elements [i0, i1) of p that 16-byte vectors cover; the up to 7
+// elements on either side are read one by one.
 template <typename T>
-__device__ double chunk_sum(const void* data, int64_t i0, int64_t i1) {
-  const T* p = reinterpret_cast<const T*>(data);
-  double s = 0.0;
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += blockDim.x) {
-    const double v = to_f32(p[i]);
-    s = fma(v, v, s);
+__device__ __forceinline__ void vector_part(const T* p, int64_t i0, int64_t i1, int64_t& v0,
+                                            int64_t& v1) {
+  constexpr int N = 16 / sizeof(T);
+  const int64_t off = (int64_t)((uintptr_t)p / sizeof(T) % N);  // element of p[0] in its vector
+  v0 = min((i0 + off + N - 1) / N * N - off, i1);
+  v1 = max((i1 + off) / N * N - off, v0);
+}
+
+__device__ __forceinline__ void add_square(double& s, float v) {
+  const double d = v;
+  s = fma(d, d, s);
+}
+
+__device__ __forceinline__ void add_squares(double (&s)[4], const uint4& u, const float*) {
+  add_square(s[0], __uint_as_float(u.x));
+  add_square(s[1], __uint_as_float(u.y));
+  add_square(s[2], __uint_as_float(u.z));
+  add_square(s[3], __uint_as_float(u.w));
+}
+__device__ __forceinline__ void add_squares(double (&s)[4], const uint4& u,
+                                            const __nv_bfloat16*) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    add_square(s[i], __uint_as_float(w[i] << 16));
+    add_square(s[i], __uint_as_float(w[i] & 0xffff0000u));
   }
-  return s;
+}
+__device__ __forceinline__ void add_squares(double (&s)[4], const uint4& u, const __half*) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    add_square(s[i], f.x);
+    add_square(s[i], f.y);
+  }
+}
+
+template <typename T>
+__device__ __noinline__ void chunk_sum(double (&s)[4], const void* data, int64_t i0, int64_t i1) {
+  constexpr int N = 16 / sizeof(T), UNROLL = 8;
+  const T* p = reinterpret_cast<const T*>(data);
+  int64_t v0, v1;
+  vector_part(p, i0, i1, v0, v1);
+  const uint4* v = reinterpret_cast<const uint4*>(p + v0);
+  const int n = (int)((v1 - v0) / N);
+  int i0v = threadIdx.x;
+  for (; i0v + (UNROLL - 1) * GL_THREADS < n; i0v += UNROLL * GL_THREADS) {
+    uint4 u[UNROLL];
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) u[k] = __ldg(v + i0v + k * GL_THREADS);
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) add_squares(s, u[k], p);
+  }
+#pragma unroll 1
+  for (; i0v < n; i0v += GL_THREADS) add_squares(s, __ldg(v + i0v), p);
+  for (int64_t i = i0 + threadIdx.x; i < v0; i += GL_THREADS) add_square(s[0], to_f32(p[i]));
+  for (int64_t i = v1 + threadIdx.x; i < i1; i += GL_THREADS) add_square(s[0], to_f32(p[i]));
 }
 
 __device__ double block_sum(double v) {
@@ -77,22 +131,22 @@ __device__ double block_sum(double v) {
   return v;
 }
 
-__global__ void __launch_bounds__(GL_THREADS)
+__global__ void __launch_bounds__(GL_THREADS, 4)
     grad_sumsq_kernel(const __grid_constant__ GradTable tb, double* __restrict__ part) {
-  double s = 0.0;
+  double acc[4] = {0.0, 0.0, 0.0, 0.0};
   for (int64_t c = blockIdx.x; c < tb.chunks; c += gridDim.x) {
     const int k = find(tb, c);
-    const int64_t i0 = (c - tb.e[k].chunk0) * GL_CHUNK;
-    const int64_t i1 = min(i0 + GL_CHUNK, tb.e[k].n);
-    if (tb.type[k] == MOE_F32) s += chunk_sum<float>(tb.e[k].data, i0, i1);
-    else if (tb.type[k] == MOE_BF16) s += chunk_sum<__nv_bfloat16>(tb.e[k].data, i0, i1);
-    else s += chunk_sum<__half>(tb.e[k].data, i0, i1);
+    const int64_t i0 = (c - tb.e[k].chunk0) * tb.chunk;
+    const int64_t i1 = min(i0 + tb.chunk, tb.e[k].n);
+    if (tb.type[k] == MOE_F32) chunk_sum<float>(acc, tb.e[k].data, i0, i1);
+    else if (tb.type[k] == MOE_BF16) chunk_sum<__nv_bfloat16>(acc, tb.e[k].data, i0, i1);
+    else chunk_sum<__half>(acc, tb.e[k].data, i0, i1);
   }
-  s = block_sum(s);
+  const double s = block_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-__global__ void __launch_bounds__(GL_THREADS)
+__global__ void __launch_bounds__(GL_THREADS, 4)
     grad_finish_kernel(const double* __restrict__ part, int64_t n, int accumulate, double* sumsq,
                        float* norm) {
   double s = 0.0;
@@ -105,14 +159,92 @@ __global__ void __launch_bounds__(GL_THREADS)
   }
 }
 
+__device__ __forceinline__ uint4 scale(const uint4& u, float f, const float*) {
+  return make_uint4(__float_as_uint(__uint_as_float(u.x) * f),
+                    __float_as_uint(__uint_as_float(u.y) * f),
+                    __float_as_uint(__uint_as_float(u.z) * f),
+                    __float_as_uint(__uint_as_float(u.w) * f));
+}
+__device__ __forceinline__ uint32_t scale2(uint32_t w, float f, const __nv_bfloat16*) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(__uint_as_float(w << 16) * f,
+                                                 __uint_as_float(w & 0xffff0000u) * f);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t scale2(uint32_t w, float f, const __half*) {
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  const __half2 r = __floats2half2_rn(v.x * f, v.y * f);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 template <typename T>
-__device__ void chunk_scale(const void* data, void* out, int64_t i0, int64_t i1, float f) {
-  const T* p = reinterpret_cast<const T*>(data);
-  T* o = reinterpret_cast<T*>(out);
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += blockDim.x) from_f32(o + i, to_f32(p[i]) * f);
+__device__ __forceinline__ uint4 scale(const uint4& u, float f, const T* t) {
+  return make_uint4(scale2(u.x, f, t), scale2(u.y, f, t), scale2(u.z, f, t), scale2(u.w, f, t));
 }
 
-__global__ void __launch_bounds__(GL_THREADS)
+// 16 bytes from byte 4 WS + bits / 8 of the 32 bytes a, b on.
+template <int WS>
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, uint32_t bits) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  return make_uint4(__funnelshift_r(w[WS], w[WS + 1], bits),
+                    __funnelshift_r(w[WS + 1], w[WS + 2], bits),
+                    __funnelshift_r(w[WS + 2], w[WS + 3], bits),
+                    __funnelshift_r(w[WS + 3], w[WS + 4], bits));
+}
+
+// Vectors of out that are 16-byte aligned, out of data that may not be: `u` points at the
+// 16 bytes that hold the first one's first element, which stands 4 WS + bits / 8 bytes in.
+// WS < 0: data is aligned too.
+template <typename T, int WS>
+__device__ __noinline__ void scale_vectors(const uint4* u, uint4* o, int n, uint32_t bits, float f) {
+  constexpr int UNROLL = WS < 0 ? 8 : 4;
+  auto load = [&](int j) {
+    if constexpr (WS < 0) return u[j];
+    else return shifted<WS>(u[j], u[j + 1], bits);  // the second from the L1: the next thread's
+  };
+  int i = threadIdx.x;
+  for (; i + (UNROLL - 1) * GL_THREADS < n; i += UNROLL * GL_THREADS) {
+    uint4 a[UNROLL];
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) a[k] = load(i + k * GL_THREADS);
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) o[i + k * GL_THREADS] = scale(a[k], f, (const T*)nullptr);
+  }
+#pragma unroll 1
+  for (; i < n; i += GL_THREADS) o[i] = scale(load(i), f, (const T*)nullptr);
+}
+
+// out[i] = f data[i] for a chunk [i0, i1) of a tensor of n elements.
+template <typename T>
+__device__ void chunk_scale(const void* data, void* out, int64_t i0, int64_t i1, int64_t n,
+                            float f) {
+  constexpr int N = 16 / sizeof(T);
+  const T* p = reinterpret_cast<const T*>(data);
+  T* o = reinterpret_cast<T*>(out);
+  int64_t v0, v1;
+  vector_part(o, i0, i1, v0, v1);
+  // where data[v0] stands in its 16 bytes; the 16-byte pieces read must lie in the tensor
+  const int in = (int)((uintptr_t)(p + v0) % 16 / sizeof(T));
+  if (in != 0 && v1 > v0) {
+    if (v0 < in) v0 += N;
+    while (v1 > v0 && v1 + N - in > n) v1 -= N;
+  }
+  if (v1 > v0) {
+    const uint4* u = reinterpret_cast<const uint4*>(p + v0 - in);
+    uint4* w = reinterpret_cast<uint4*>(o + v0);
+    const int nv = (int)((v1 - v0) / N);
+    const uint32_t byte = in * sizeof(T), bits = byte % 4 * 8;
+    if (byte == 0) scale_vectors<T, -1>(u, w, nv, 0, f);
+    else if (byte < 4) scale_vectors<T, 0>(u, w, nv, bits, f);
+    else if (byte < 8) scale_vectors<T, 1>(u, w, nv, bits, f);
+    else if (byte < 12) scale_vectors<T, 2>(u, w, nv, bits, f);
+    else scale_vectors<T, 3>(u, w, nv, bits, f);
+  } else {
+    v0 = v1 = i1;
+  }
+  for (int64_t i = i0 + threadIdx.x; i < v0; i += GL_THREADS) from_f32(o + i, to_f32(p[i]) * f);
+  for (int64_t i = v1 + threadIdx.x; i < i1; i += GL_THREADS) from_f32(o + i, to_f32(p[i]) * f);
+}
+
+__global__ void __launch_bounds__(GL_THREADS, 4)
     grad_clip_kernel(const __grid_constant__ GradTable tb, const double* __restrict__ sumsq,
                      float max_norm, float* norm, float* coef) {
   const double nm = sqrt(*sumsq);
@@ -126,18 +258,18 @@ __global__ void __launch_bounds__(GL_THREADS)
     const int k = find(tb, c);
     const GradEnt& e = tb.e[k];
     if (f == 1.0f && e.out == e.data) continue;
-    const int64_t i0 = (c - e.chunk0) * GL_CHUNK;
-    const int64_t i1 = min(i0 + GL_CHUNK, e.n);
-    if (tb.type[k] == MOE_F32) chunk_scale<float>(e.data, e.out, i0, i1, f);
-    else if (tb.type[k] == MOE_BF16) chunk_scale<__nv_bfloat16>(e.data, e.out, i0, i1, f);
-    else chunk_scale<__half>(e.data, e.out, i0, i1, f);
+    const int64_t i0 = (c - e.chunk0) * tb.chunk;
+    const int64_t i1 = min(i0 + tb.chunk, e.n);
+    if (tb.type[k] == MOE_F32) chunk_scale<float>(e.data, e.out, i0, i1, e.n, f);
+    else if (tb.type[k] == MOE_BF16) chunk_scale<__nv_bfloat16>(e.data, e.out, i0, i1, e.n, f);
+    else chunk_scale<__half>(e.data, e.out, i0, i1, e.n, f);
   }
 }
 
 // The next launch's table: tensors from *i on, empty ones left out.
 void fill(GradTable& tb, const moe_grad* g, int64_t n, int64_t* i) {
   tb.n = 0;
-  tb.chunks = 0;
+  int64_t total = 0;
   for (; *i < n && tb.n < GL_MAX; ++*i) {
     const moe_grad& x = g[*i];
     if (x.n == 0) continue;
@@ -145,9 +277,15 @@ void fill(GradTable& tb, const moe_grad* g, int64_t n, int64_t* i) {
     e.data = x.data;
     e.out = x.out ? x.out : const_cast<void*>(x.data);
     e.n = x.n;
-    e.chunk0 = tb.chunks;
+    total += x.n;
     tb.type[tb.n++] = (uint8_t)x.type;
-    tb.chunks += (x.n + GL_CHUNK - 1) / GL_CHUNK;
+  }
+  tb.chunk = GL_CHUNK;
+  while (tb.chunk > GL_CHUNK_MIN && total / tb.chunk < GL_CTAS) tb.chunk /= 2;
+  tb.chunks = 0;
+  for (int k = 0; k < tb.n; ++k) {
+    tb.e[k].chunk0 = tb.chunks;
+    tb.chunks += (tb.e[k].n + tb.chunk - 1) / tb.chunk;
   }
 }
 
