@@ -142,16 +142,21 @@ __global__ void __launch_bounds__(GL_THREADS, 4)
     else if (tb.type[k] == MOE_BF16) chunk_sum<__nv_bfloat16>(acc, tb.e[k].data, i0, i1);
     else chunk_sum<__half>(acc, tb.e[k].data, i0, i1);
   }
+  cudaTriggerProgrammaticLaunchCompletion();  // the clipping's CTAs may come in as these leave
   const double s = block_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-__global__ void __launch_bounds__(GL_THREADS, 4)
-    grad_finish_kernel(const double* __restrict__ part, int64_t n, int accumulate, double* sumsq,
-                       float* norm) {
+// The norm launches' partial sums, the same bits in every CTA that adds them.
+__device__ __forceinline__ double sum_parts(const double* part, int64_t n) {
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += blockDim.x) s += part[i];
-  s = block_sum(s);
+  for (int64_t i = threadIdx.x; i < n; i += GL_THREADS) s += part[i];
+  return block_sum(s);
+}
+
+__global__ void __launch_bounds__(GL_THREADS)
+    grad_finish_kernel(const double* part, int64_t n, int accumulate, double* sumsq, float* norm) {
+  double s = sum_parts(part, n);
   if (threadIdx.x == 0) {
     if (accumulate) s += *sumsq;
     *sumsq = s;
@@ -244,17 +249,24 @@ __device__ void chunk_scale(const void* data, void* out, int64_t i0, int64_t i1,
   for (int64_t i = v1 + threadIdx.x; i < i1; i += GL_THREADS) from_f32(o + i, to_f32(p[i]) * f);
 }
 
+// parts > 0: the sum of squares is that of the norm launches' partial sums, which every
+// CTA adds up for itself, and is written to sumsq; otherwise sumsq is given.  The chunks
+// are taken in the reverse of the norm's order: what it read last may still be in the L2.
 __global__ void __launch_bounds__(GL_THREADS, 4)
-    grad_clip_kernel(const __grid_constant__ GradTable tb, const double* __restrict__ sumsq,
-                     float max_norm, float* norm, float* coef) {
-  const double nm = sqrt(*sumsq);
+    grad_clip_kernel(const __grid_constant__ GradTable tb, const double* part, int64_t parts,
+                     double* sumsq, float max_norm, float* norm, float* coef) {
+  cudaGridDependencySynchronize();  // launched while the norm's last CTAs still ran
+  const double ss = parts > 0 ? sum_parts(part, parts) : *sumsq;
+  const double nm = sqrt(ss);
   const double q = (double)max_norm / (nm + 1e-6);
   const float f = q >= 1.0 ? 1.0f : (float)q;  // a NaN stays one
   if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (parts > 0) *sumsq = ss;
     if (norm) *norm = (float)nm;
     if (coef) *coef = f;
   }
-  for (int64_t c = blockIdx.x; c < tb.chunks; c += gridDim.x) {
+  for (int64_t r = blockIdx.x; r < tb.chunks; r += gridDim.x) {
+    const int64_t c = tb.chunks - 1 - r;
     const int k = find(tb, c);
     const GradEnt& e = tb.e[k];
     if (f == 1.0f && e.out == e.data) continue;
@@ -297,10 +309,8 @@ size_t grad_ws_bytes(int64_t n) {
   return align_up((size_t)grad_launches(n) * GL_CTAS * sizeof(double), 256);
 }
 
-int launch_grad_norm(const moe_grad* g, int64_t n, int accumulate, double* sumsq, float* norm,
-                     void* ws, void* stream) {
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  double* part = reinterpret_cast<double*>(ws);
+// The norm's launches over a list; returns how many partial sums they leave in part.
+static int64_t sumsq_launches(const moe_grad* g, int64_t n, double* part, cudaStream_t st) {
   int64_t parts = 0;
   for (int64_t i = 0; i < n;) {
     GradTable tb;
@@ -310,21 +320,60 @@ int launch_grad_norm(const moe_grad* g, int64_t n, int accumulate, double* sumsq
     grad_sumsq_kernel<<<ctas, GL_THREADS, 0, st>>>(tb, part + parts);
     parts += ctas;
   }
+  return parts;
+}
+
+int launch_grad_norm(const moe_grad* g, int64_t n, int accumulate, double* sumsq, float* norm,
+                     void* ws, void* stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  double* part = reinterpret_cast<double*>(ws);
+  const int64_t parts = sumsq_launches(g, n, part, st);
   grad_finish_kernel<<<1, GL_THREADS, 0, st>>>(part, parts, accumulate, sumsq, norm);
   return cuda_ok(cudaGetLastError()) ? MOE_OK : MOE_ERR_CUDA;
 }
 
-int launch_grad_clip(const moe_grad* g, int64_t n, const double* sumsq, float max_norm,
-                     float* norm, float* coef, void* stream) {
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+// The clipping's launches, last tensors first.  parts > 0: after the norm's, by its
+// partial sums.
+static int clip_launches(const moe_grad* g, int64_t n, const double* part, int64_t parts,
+                         double* sumsq, float max_norm, float* norm, float* coef,
+                         cudaStream_t st) {
+  bool first = true;
   int64_t i = 0;
   do {
     GradTable tb;
     fill(tb, g, n, &i);
     const int64_t ctas = tb.chunks < GL_CTAS ? (tb.chunks > 0 ? tb.chunks : 1) : GL_CTAS;
-    grad_clip_kernel<<<(unsigned)ctas, GL_THREADS, 0, st>>>(tb, sumsq, max_norm, norm, coef);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(GL_THREADS);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = parts > 0 && first ? 1 : 0;  // directly behind a launch of the norm's
+    if (!cuda_ok(cudaLaunchKernelEx(&cfg, grad_clip_kernel, tb, part, parts, sumsq, max_norm,
+                                    norm, coef)))
+      return MOE_ERR_CUDA;
+    first = false;
   } while (i < n);
-  return cuda_ok(cudaGetLastError()) ? MOE_OK : MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+int launch_grad_clip(const moe_grad* g, int64_t n, const double* sumsq, float max_norm,
+                     float* norm, float* coef, void* stream) {
+  return clip_launches(g, n, nullptr, 0, const_cast<double*>(sumsq), max_norm, norm, coef,
+                       reinterpret_cast<cudaStream_t>(stream));
+}
+
+int launch_grad_clip_norm(const moe_grad* g, int64_t n, float max_norm, double* sumsq,
+                          float* norm, float* coef, void* ws, void* stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  double* part = reinterpret_cast<double*>(ws);
+  const int64_t parts = sumsq_launches(g, n, part, st);
+  if (!cuda_ok(cudaGetLastError())) return MOE_ERR_CUDA;
+  if (parts == 0 && !cuda_ok(cudaMemsetAsync(sumsq, 0, sizeof(double), st))) return MOE_ERR_CUDA;
+  return clip_launches(g, n, part, parts, sumsq, max_norm, norm, coef, st);
 }
 
 }  // namespace moe

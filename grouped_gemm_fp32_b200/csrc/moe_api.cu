@@ -295,13 +295,11 @@ int moe_grad_clip(const moe_grad* grads, int64_t n_grads, const double* sumsq, f
 
 int moe_grad_clip_norm(const moe_grad* grads, int64_t n_grads, float max_norm, double* sumsq,
                        float* norm, float* coef, void* ws, size_t ws_bytes, void* stream) {
-  int rc = check_grads(grads, n_grads);
+  const int rc = check_grads(grads, n_grads);
   if (rc) return rc;
   if (!sumsq || !(max_norm >= 0.0f) || !ws || ws_bytes < grad_ws_bytes(n_grads))
     return MOE_ERR_INVALID_ARG;
-  rc = launch_grad_norm(grads, n_grads, 0, sumsq, nullptr, ws, stream);
-  if (rc) return rc;
-  return launch_grad_clip(grads, n_grads, sumsq, max_norm, norm, coef, stream);
+  return launch_grad_clip_norm(grads, n_grads, max_norm, sumsq, norm, coef, ws, stream);
 }
 
 int moe_bias_update(const moe_dims* dims, const int32_t* counts, float gamma,

@@ -206,6 +206,8 @@ int launch_grad_norm(const moe_grad* g, int64_t n, int accumulate, double* sumsq
                      void* ws, void* stream);
 int launch_grad_clip(const moe_grad* g, int64_t n, const double* sumsq, float max_norm,
                      float* norm, float* coef, void* stream);
+int launch_grad_clip_norm(const moe_grad* g, int64_t n, float max_norm, double* sumsq,
+                          float* norm, float* coef, void* ws, void* stream);
 
 enum GemmMode { MODE_FWD1 = 0, MODE_FWD2, MODE_DX2, MODE_DX1, MODE_DW2, MODE_DW1 };
 
