@@ -3,22 +3,47 @@
 // pages have no counterpart).
 //
 // HBM-bound: forward y, res -> u, n; backward dn, du, y, u -> dy, dres, every
-// element once, a row in registers between its statistics and its outputs.
+// element once.  Persistent CTAs walk a contiguous range of rows each, a row spread
+// over the CTA's threads, eight columns a vector.  Rows come in by cp.async into a ring
+// in shared memory, several rows ahead; a thread copies and reads its own columns only,
+// so a row costs one barrier a statistic and none for its data.  The weights stay in
+// registers (rows of up to 8192 columns), and so do the backward's sums over tokens.
 //
 // The backward's statistics are one round of six row sums.  With a = dn w_pre,
 // q = beta gate w_post y, r = 1 / rms(u) and du = d + r a - c u, c = r^3 <a, u> / d:
 //   <q, du> = <q, d> + r <q, a> - c <q, u>
 // so <u, u>, <a, u>, <y, y>, <q, d>, <q, a>, <q, u> give dy's mean as well.
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "moe_internal.cuh"
+#include "sm100.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int NB_CTAS = 148;  // backward: CTAs (row ranges), one partial row of each sum per CTA
-constexpr int NV = 8;         // columns per vector
+constexpr int NB_SMS = 148;       // SMs of a B200; CTAs are a multiple of it
+constexpr int NB_STAGES = 8;      // most rows in a ring
+constexpr int NB_SMEM = 226 * 1024;  // an SM's shared memory for its CTAs' rings
+constexpr int NV = 8;             // columns per vector
+
+// How rows of d columns are spread over a CTA: V vectors a thread, and how many CTAs
+// share an SM (512 threads an SM; fewer threads than that leave the copies in flight, not
+// the arithmetic, to fill it).
+struct Shape {
+  int v, threads, per_sm;
+};
+Shape shape_of(int d) {
+  const int nvec = d / NV;
+  Shape s;
+  s.v = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
+  s.threads = ((nvec + s.v - 1) / s.v + 31) / 32 * 32;
+  s.per_sm = 512 / s.threads;
+  if (s.per_sm > 16) s.per_sm = 16;
+  return s;
+}
 
 struct F8 {
   float v[NV];
@@ -54,25 +79,62 @@ __device__ __forceinline__ void st8(float* p, const F8& r) {
   reinterpret_cast<float4*>(p)[1] = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
 }
 
-// Sums of N values over the CTA, the same bits in every thread.
+// Sums of N values over the CTA, the same bits in every thread.  Calls alternate between
+// two halves of sh [2][16][N], so one barrier a call is enough.
 template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N]) {
-  __shared__ float sh[32][N];
+__device__ __forceinline__ void block_sum(float (&v)[N], float* sh, int& half) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  float* mine = sh + half * 16 * N;
+  half ^= 1;
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  __syncthreads();  // the previous call's values have been read
   if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) sh[warp][i] = v[i];
+    for (int i = 0; i < N; ++i) mine[warp * N + i] = v[i];
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = 0.0f;
-    for (int w = 0; w < nw; ++w) v[i] += sh[w][i];
+  for (int i = 0; i < N; ++i) v[i] = mine[i];
+  for (int w = 1; w < nw; ++w)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += mine[w * N + i];
+}
+
+__device__ __forceinline__ void cp16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most n of this thread's copy groups are still in flight.
+__device__ __forceinline__ void cp_wait(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
   }
+}
+
+// One matrix's row in a ring stage: 16 bytes a vector in bf16, two pieces of 16 in FP32,
+// the first pieces of all vectors before the second ones.
+__device__ __forceinline__ void cp_row(uint4* st, int nvec, int c, const __nv_bfloat16* g) {
+  cp16(st + c, g);
+}
+__device__ __forceinline__ void cp_row(uint4* st, int nvec, int c, const float* g) {
+  cp16(st + c, g);
+  cp16(st + nvec + c, g + 4);
+}
+__device__ __forceinline__ F8 rd_row(const uint4* st, int nvec, int c, const __nv_bfloat16*) {
+  return ld8(reinterpret_cast<const __nv_bfloat16*>(st + c));
+}
+__device__ __forceinline__ F8 rd_row(const uint4* st, int nvec, int c, const float*) {
+  const float4 a = *reinterpret_cast<const float4*>(st + c);
+  const float4 b = *reinterpret_cast<const float4*>(st + nvec + c);
+  return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
 }
 
 struct FwdK {
@@ -81,86 +143,154 @@ struct FwdK {
   const float *w_post, *gate, *w_pre;
   void* u;
   __nv_bfloat16* n;
-  int64_t seq_len;  // 0: one gate row
-  int d;
+  int64_t T, rows, seq_len;  // rows: tokens per CTA; seq_len >= 1
+  int d, stages;
   float eps, alpha, beta;
 };
 
-template <typename RT, int V>
-__global__ void block_norm_kernel(const FwdK a) {
-  const int64_t t = blockIdx.x;
-  const int nvec = a.d / NV;
-  const RT* res = reinterpret_cast<const RT*>(a.res) + t * a.d;
-  F8 u[V], y[V];
+// beta gate w_post of a vector (w_post and gate may be NULL).
+__device__ __forceinline__ F8 post_factor(const float* w_post, const float* gate, float beta,
+                                          int c) {
+  F8 f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
-    if (c < nvec) {
-      u[i] = ld8(res + c * NV);
-      if (a.y) y[i] = ld8(a.y + t * a.d + c * NV);
-    }
+  for (int j = 0; j < NV; ++j) f.v[j] = beta;
+  if (w_post) {
+    const F8 w = ld8(w_post + c * NV);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) f.v[j] *= w.v[j];
   }
-  if (a.y) {
-    float r1 = 1.0f;
-    if (a.w_post) {
-      float s[1] = {0.0f};
+  if (gate) {
+    const F8 g = ld8(gate + c * NV);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) f.v[j] *= g.v[j];
+  }
+  return f;
+}
+
+template <typename RT, int V, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(const FwdK a) {
+  constexpr bool KEEP = V <= 2;  // the weights in registers; else read again every row
+  constexpr int R = sizeof(RT) / 2;
+  extern __shared__ uint4 ring[];
+  __shared__ float sh[2 * 16];
+  int half = 0;
+  const int nvec = a.d / NV, tid = threadIdx.x, nt = blockDim.x;
+  const int64_t t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
+  const int S = a.stages, row_v = (1 + R) * nvec;  // a stage: y, then res
+  const RT* res = reinterpret_cast<const RT*>(a.res);
+  RT* u_out = reinterpret_cast<RT*>(a.u);
+  int put = 0, get = 0;  // ring stages of the next row to copy and to read
+  auto issue = [&](int64_t t) {
+    if (t < t1) {
+      uint4* st = ring + (size_t)put * row_v;
+      put = put + 1 == S ? 0 : put + 1;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nt;
+        if (c >= nvec) continue;
+        const int64_t at = t * a.d + c * NV;
+        if (a.y) cp_row(st, nvec, c, a.y + at);
+        cp_row(st + nvec, nvec, c, res + at);
+      }
+    }
+    cp_commit();
+  };
+  for (int s = 0; s + 1 < S; ++s) issue(t0 + s);
+  F8 f[KEEP ? V : 1], wp[KEEP ? V : 1];
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (a.w_pre && tid + i * nt < nvec) wp[i] = ld8(a.w_pre + (tid + i * nt) * NV);
+  }
+  int64_t seq_end = t0;  // first token past the gate row that f holds
+  const float* gate = nullptr;
+  for (int64_t t = t0; t < t1; ++t) {
+    if (t >= seq_end) {
+      const int64_t s = t / a.seq_len;
+      seq_end = (s + 1) * a.seq_len;
+      if (a.gate) gate = a.gate + s * a.d;
+      if constexpr (KEEP) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (a.y && tid + i * nt < nvec)
+            f[i] = post_factor(a.w_post, gate, a.beta, tid + i * nt);
+      }
+    }
+    if (S == 1) {
+      __syncthreads();
+      issue(t);
+    }
+    cp_wait(S > 1 ? S - 2 : 0);
+    const uint4* st = ring + (size_t)get * row_v;
+    get = get + 1 == S ? 0 : get + 1;
+    F8 u[V];
+    float s[1] = {0.0f};
+    if (a.y) {
+      F8 y[V];
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (threadIdx.x + i * blockDim.x < nvec)
+        if (tid + i * nt < nvec) {
+          y[i] = rd_row(st, nvec, tid + i * nt, a.y);
 #pragma unroll
           for (int j = 0; j < NV; ++j) s[0] = fmaf(y[i].v[j], y[i].v[j], s[0]);
-      block_sum<1>(s);
-      r1 = rsqrtf(s[0] / a.d + a.eps);
-    }
-    const float* gate = a.gate ? a.gate + (a.seq_len ? t / a.seq_len : 0) * a.d : nullptr;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = threadIdx.x + i * blockDim.x;
-      if (c >= nvec) continue;
-      F8 f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) f.v[j] = a.beta * r1;
+        }
+      float r1 = 1.0f;
       if (a.w_post) {
-        const F8 w = ld8(a.w_post + c * NV);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) f.v[j] *= w.v[j];
+        block_sum<1>(s, sh, half);
+        r1 = rsqrtf(s[0] / a.d + a.eps);
       }
-      if (gate) {
-        const F8 g = ld8(gate + c * NV);
+      s[0] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) f.v[j] *= g.v[j];
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nt;
+        if (c >= nvec) continue;
+        u[i] = rd_row(st + nvec, nvec, c, res);
+        const F8 g = KEEP ? f[KEEP ? i : 0] : post_factor(a.w_post, gate, a.beta, c);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          u[i].v[j] = fmaf(g.v[j] * r1, y[i].v[j], a.alpha * u[i].v[j]);
+          s[0] = fmaf(u[i].v[j], u[i].v[j], s[0]);
+        }
+        st8(u_out + t * a.d + c * NV, u[i]);
       }
+    } else {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) u[i].v[j] = fmaf(f.v[j], y[i].v[j], a.alpha * u[i].v[j]);
-      st8(reinterpret_cast<RT*>(a.u) + t * a.d + c * NV, u[i]);
+      for (int i = 0; i < V; ++i)
+        if (tid + i * nt < nvec) {
+          u[i] = rd_row(st + nvec, nvec, tid + i * nt, res);
+#pragma unroll
+          for (int j = 0; j < NV; ++j) s[0] = fmaf(u[i].v[j], u[i].v[j], s[0]);
+        }
     }
-  }
-  if (a.n == nullptr) return;
-  float s[1] = {0.0f};
+    // a copy refills the stage of the row before this one: every thread has passed a
+    // barrier since it read that
+    if (a.n) {
+      block_sum<1>(s, sh, half);
+      if (S > 1) issue(t + S - 1);
+      const float r2 = rsqrtf(s[0] / a.d + a.eps);
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (threadIdx.x + i * blockDim.x < nvec)
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nt;
+        if (c >= nvec) continue;
+        F8 w = KEEP ? wp[KEEP ? i : 0] : ld8(a.w_pre + c * NV);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) s[0] = fmaf(u[i].v[j], u[i].v[j], s[0]);
-  block_sum<1>(s);
-  const float r2 = rsqrtf(s[0] / a.d + a.eps);
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
-    if (c >= nvec) continue;
-    F8 w = ld8(a.w_pre + c * NV);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) w.v[j] *= u[i].v[j] * r2;
-    st8(a.n + t * a.d + c * NV, w);
+        for (int j = 0; j < NV; ++j) w.v[j] *= u[i].v[j] * r2;
+        st8(a.n + t * a.d + c * NV, w);
+      }
+    } else {
+      if (!a.w_post) __syncthreads();  // as a statistic's barrier
+      if (S > 1) issue(t + S - 1);
+    }
   }
 }
 
-// Backward workspace: per CTA one row of each of the sums over its tokens --
-//   post [NB_CTAS][d]  sum_t gate du y / rms(y)          -> dw_post
-//   pre  [NB_CTAS][d]  sum_t dn u / rms(u)               -> dw_pre
-//   seq  [NB_CTAS + sequences][d]  sum_t du y / rms(y) over the CTA's tokens of one
-//        gate row, at row CTA + gate row (both grow along the tokens, so no two
-//        pieces share a row)                             -> dgate
+// Backward workspace, with C the CTAs: per CTA one row of each of the sums over its
+// tokens --
+//   post [C][d]  sum_t gate du y / rms(y)          -> dw_post
+//   pre  [C][d]  sum_t dn u / rms(u)               -> dw_pre
+//   seq  [C + sequences][d]  sum_t du y / rms(y) over the CTA's tokens of one gate row,
+//        at row CTA + gate row (both grow along the tokens, so no two pieces share a
+//        row)                                      -> dgate
 struct BwdK {
   const __nv_bfloat16 *dn, *y;
   const void *du, *u;
@@ -169,113 +299,183 @@ struct BwdK {
   void* dres;
   float *post, *pre, *seq;
   int64_t T, rows, seq_len;  // rows: tokens per CTA; seq_len >= 1
-  int d;
+  int d, stages;
   float eps, alpha, beta;
 };
 
-template <typename RT, int V>
-__global__ void __launch_bounds__(512) block_norm_bwd_kernel(const BwdK a) {
-  const int nvec = a.d / NV;
+template <typename RT, int V, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(const BwdK a) {
+  constexpr bool KEEP = V <= 2;
+  constexpr int R = sizeof(RT) / 2;
+  extern __shared__ uint4 ring[];
+  __shared__ float sh[2 * 16 * 6];
+  int half = 0;
+  const int nvec = a.d / NV, tid = threadIdx.x, nt = blockDim.x;
   const int64_t t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
-  F8 sa[V], sp[V], sb[V];
+  const int S = a.stages, row_v = (2 + 2 * R) * nvec;  // a stage: dn, y, dres_out, u
+  const RT* du_in = reinterpret_cast<const RT*>(a.du);
+  const RT* u_in = reinterpret_cast<const RT*>(a.u);
+  RT* dres_out = reinterpret_cast<RT*>(a.dres);
+  int put = 0, get = 0;  // ring stages of the next row to copy and to read
+  auto issue = [&](int64_t t) {
+    if (t < t1) {
+      uint4* st = ring + (size_t)put * row_v;
+      put = put + 1 == S ? 0 : put + 1;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nt;
+        if (c >= nvec) continue;
+        const int64_t at = t * a.d + c * NV;
+        if (a.dn) {
+          cp_row(st, nvec, c, a.dn + at);
+          cp_row(st + (2 + R) * nvec, nvec, c, u_in + at);
+        }
+        if (a.y) cp_row(st + nvec, nvec, c, a.y + at);
+        if (a.du) cp_row(st + 2 * nvec, nvec, c, du_in + at);
+      }
+    }
+    cp_commit();
+  };
+  // matrices that are not there read as zeros: no copy ever writes their part of the ring
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * nt;
+      if (c >= nvec) continue;
+      uint4* st = ring + (size_t)s * row_v;
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      if (!a.dn) {
+        st[c] = z;
+#pragma unroll
+        for (int r = 0; r < R; ++r) st[(2 + R + r) * nvec + c] = z;
+      }
+      if (!a.y) st[nvec + c] = z;
+      if (!a.du) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) st[(2 + r) * nvec + c] = z;
+      }
+    }
+  for (int s = 0; s + 1 < S; ++s) issue(t0 + s);
+  F8 sa[V], sb[V], f[KEEP ? V : 1], wp[KEEP ? V : 1];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int j = 0; j < NV; ++j) sa[i].v[j] = sp[i].v[j] = sb[i].v[j] = 0.0f;
+    for (int j = 0; j < NV; ++j) sa[i].v[j] = sb[i].v[j] = 0.0f;
+  const F8 zero = sa[0];
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      wp[i] = a.dn && tid + i * nt < nvec ? ld8(a.w_pre + (tid + i * nt) * NV) : zero;
+  }
+  const float inv_d = 1.0f / a.d, alpha = a.y ? a.alpha : 1.0f;
+  int64_t seq_end = t0, seq = 0;  // the gate row that f holds, and the first token past it
+  const float* gate = nullptr;
+  bool flushed = false;  // post holds the sums of earlier gate rows
   for (int64_t t = t0; t < t1; ++t) {
-    const int64_t s = t / a.seq_len;
-    const float* gate = a.gate ? a.gate + s * a.d : nullptr;
-    F8 du[V], u[V], an[V], y[V], q[V], dn[V];
+    if (t >= seq_end) {
+      seq = t / a.seq_len;
+      seq_end = (seq + 1) * a.seq_len;
+      if (a.gate) gate = a.gate + seq * a.d;
+      if constexpr (KEEP) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          f[i] = a.y && tid + i * nt < nvec ? post_factor(a.w_post, gate, a.beta, tid + i * nt)
+                                            : zero;
+      }
+    }
+    if (S == 1) {
+      __syncthreads();
+      issue(t);
+    }
+    cp_wait(S > 1 ? S - 2 : 0);
+    const uint4* st = ring + (size_t)get * row_v;
+    get = get + 1 == S ? 0 : get + 1;
     float sum[6] = {0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = threadIdx.x + i * blockDim.x;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        du[i].v[j] = u[i].v[j] = an[i].v[j] = y[i].v[j] = q[i].v[j] = dn[i].v[j] = 0.0f;
+      const int c = tid + i * nt;
       if (c >= nvec) continue;
-      const int64_t at = t * a.d + c * NV;
-      if (a.du) du[i] = ld8(reinterpret_cast<const RT*>(a.du) + at);
-      if (a.dn) {
-        u[i] = ld8(reinterpret_cast<const RT*>(a.u) + at);
-        dn[i] = ld8(a.dn + at);
-        const F8 w = ld8(a.w_pre + c * NV);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) an[i].v[j] = dn[i].v[j] * w.v[j];
-      }
-      if (a.y) {
-        y[i] = ld8(a.y + at);
-        F8 f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) f.v[j] = a.beta;
-        if (a.w_post) {
-          const F8 w = ld8(a.w_post + c * NV);
-#pragma unroll
-          for (int j = 0; j < NV; ++j) f.v[j] *= w.v[j];
-        }
-        if (gate) {
-          const F8 g = ld8(gate + c * NV);
-#pragma unroll
-          for (int j = 0; j < NV; ++j) f.v[j] *= g.v[j];
-        }
-        q[i] = f;
+      const F8 dn = rd_row(st, nvec, c, a.dn), y = rd_row(st + nvec, nvec, c, a.y);
+      const F8 du = rd_row(st + 2 * nvec, nvec, c, du_in);
+      const F8 u = rd_row(st + (2 + R) * nvec, nvec, c, u_in);
+      F8 g, w;
+      if constexpr (KEEP) {
+        g = f[i];
+        w = wp[i];
+      } else {
+        g = a.y ? post_factor(a.w_post, gate, a.beta, c) : zero;
+        w = a.dn ? ld8(a.w_pre + c * NV) : zero;
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const float qy = q[i].v[j] * y[i].v[j];
-        sum[0] = fmaf(u[i].v[j], u[i].v[j], sum[0]);
-        sum[1] = fmaf(an[i].v[j], u[i].v[j], sum[1]);
-        sum[2] = fmaf(y[i].v[j], y[i].v[j], sum[2]);
-        sum[3] = fmaf(qy, du[i].v[j], sum[3]);
-        sum[4] = fmaf(qy, an[i].v[j], sum[4]);
-        sum[5] = fmaf(qy, u[i].v[j], sum[5]);
+        const float an = dn.v[j] * w.v[j], qy = g.v[j] * y.v[j];
+        sum[0] = fmaf(u.v[j], u.v[j], sum[0]);
+        sum[1] = fmaf(an, u.v[j], sum[1]);
+        sum[2] = fmaf(y.v[j], y.v[j], sum[2]);
+        sum[3] = fmaf(qy, du.v[j], sum[3]);
+        sum[4] = fmaf(qy, an, sum[4]);
+        sum[5] = fmaf(qy, u.v[j], sum[5]);
       }
     }
-    block_sum<6>(sum);
-    const float inv_d = 1.0f / a.d;
-    const float r2 = rsqrtf(fmaf(sum[0], inv_d, a.eps));
+    block_sum<6>(sum, sh, half);
+    // the stage of the row before this one: every thread has passed a barrier since it read it
+    if (S > 1) issue(t + S - 1);
+    const float r2 = a.dn ? rsqrtf(fmaf(sum[0], inv_d, a.eps)) : 0.0f;
     const float c2 = r2 * r2 * r2 * sum[1] * inv_d;
     const float r1 = a.w_post ? rsqrtf(fmaf(sum[2], inv_d, a.eps)) : 1.0f;
     const float c1 =
         a.w_post ? r1 * r1 * r1 * inv_d * (sum[3] + r2 * sum[4] - c2 * sum[5]) : 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = threadIdx.x + i * blockDim.x;
+      const int c = tid + i * nt;
       if (c >= nvec) continue;
-      const int64_t at = t * a.d + c * NV;
-      F8 g;
-      if (gate) g = ld8(gate + c * NV);
-      F8 dres, dy;
+      const F8 dn = rd_row(st, nvec, c, a.dn), y = rd_row(st + nvec, nvec, c, a.y);
+      const F8 du = rd_row(st + 2 * nvec, nvec, c, du_in);
+      const F8 u = rd_row(st + (2 + R) * nvec, nvec, c, u_in);
+      F8 g, w, dres, dy;
+      if constexpr (KEEP) {
+        g = f[i];
+        w = wp[i];
+      } else {
+        g = a.y ? post_factor(a.w_post, gate, a.beta, c) : zero;
+        w = a.dn ? ld8(a.w_pre + c * NV) : zero;
+      }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const float du_j = du[i].v[j] + (a.dn ? r2 * an[i].v[j] - c2 * u[i].v[j] : 0.0f);
-        dres.v[j] = a.y ? a.alpha * du_j : du_j;
-        dy.v[j] = r1 * q[i].v[j] * du_j - c1 * y[i].v[j];
-        const float x = du_j * (r1 * y[i].v[j]);
-        sa[i].v[j] += x;
-        sp[i].v[j] += gate ? g.v[j] * x : x;
-        sb[i].v[j] += dn[i].v[j] * (r2 * u[i].v[j]);
+        const float v = du.v[j] + (r2 * (dn.v[j] * w.v[j]) - c2 * u.v[j]);
+        dres.v[j] = alpha * v;
+        const float x = r1 * v;
+        dy.v[j] = g.v[j] * x - c1 * y.v[j];
+        sa[i].v[j] = fmaf(x, y.v[j], sa[i].v[j]);
+        sb[i].v[j] = fmaf(dn.v[j], r2 * u.v[j], sb[i].v[j]);
       }
-      st8(reinterpret_cast<RT*>(a.dres) + at, dres);
+      const int64_t at = t * a.d + c * NV;
+      st8(dres_out + at, dres);
       if (a.y) st8(a.dy + at, dy);
     }
-    if (a.seq && (t + 1 == t1 || (t + 1) / a.seq_len != s)) {
+    if (t + 1 == t1 || t + 1 == seq_end) {  // the gate row's sums are complete here
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if (c < nvec) st8(a.seq + ((int64_t)blockIdx.x + s) * a.d + c * NV, sa[i]);
+        const int c = tid + i * nt;
+        if (c >= nvec) continue;
+        if (a.seq) st8(a.seq + ((int64_t)blockIdx.x + seq) * a.d + c * NV, sa[i]);
+        if (a.post) {
+          float* p = a.post + (int64_t)blockIdx.x * a.d + c * NV;
+          F8 v = flushed ? ld8(p) : zero;
+          const F8 g = gate ? ld8(gate + c * NV) : zero;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) sa[i].v[j] = 0.0f;
+          for (int j = 0; j < NV; ++j) v.v[j] += gate ? g.v[j] * sa[i].v[j] : sa[i].v[j];
+          st8(p, v);
+        }
+        sa[i] = zero;
       }
+      flushed = true;
     }
   }
+  if (a.pre)
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
-    if (c >= nvec) continue;
-    if (a.post) st8(a.post + (int64_t)blockIdx.x * a.d + c * NV, sp[i]);
-    if (a.pre) st8(a.pre + (int64_t)blockIdx.x * a.d + c * NV, sb[i]);
-  }
+    for (int i = 0; i < V; ++i)
+      if (tid + i * nt < nvec) st8(a.pre + (int64_t)blockIdx.x * a.d + (tid + i * nt) * NV, sb[i]);
 }
 
 struct FinK {
@@ -330,33 +530,75 @@ int64_t gate_rows(const moe_dims& dm, const moe_norm_cfg& c) {
   return c.seq_len && dm.T ? (dm.T + c.seq_len - 1) / c.seq_len : 1;
 }
 
-template <typename RT, int V>
-void fwd(const FwdK& k, int64_t T, int threads, cudaStream_t st) {
-  block_norm_kernel<RT, V><<<(unsigned)T, threads, 0, st>>>(k);
+// CTAs of a launch over T rows and the rows each takes.
+int64_t split_rows(int64_t T, int d, int64_t* rows) {
+  const int64_t most = (int64_t)NB_SMS * shape_of(d).per_sm;
+  *rows = T ? (T + most - 1) / most : 1;
+  return (T + *rows - 1) / *rows;
+}
+
+// Raises a kernel's shared-memory limit, once per device (a bit of `ready` each).
+template <typename K>
+bool opt_in(void (*kernel)(const K), std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  if (!cuda_ok(cudaGetDevice(&dev))) return false;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (ready.load(std::memory_order_relaxed) & bit) return true;
+  if (!cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    NB_SMEM - 1536)))
+    return false;
+  ready.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
+// Launch on rows of `pieces` 16-byte pieces a vector: the ring takes what its CTA's share
+// of the SM's shared memory holds, the CTA's rows at most.
+template <typename K>
+int launch_rows(void (*kernel)(const K), std::atomic<uint64_t>& ready, K k, int pieces,
+                int64_t ctas, cudaStream_t st) {
+  const Shape s = shape_of(k.d);
+  const int64_t stage = (int64_t)pieces * (k.d / NV) * 16;
+  int64_t n = (NB_SMEM / s.per_sm - 1536) / stage;  // 1 KB a CTA and the static part beside it
+  if (n > NB_STAGES) n = NB_STAGES;
+  if (n > k.rows + 1) n = k.rows + 1;
+  if (n < 1) n = 1;
+  k.stages = (int)n;
+  const int bytes = (int)(n * stage);
+  if (!opt_in(kernel, ready)) return MOE_ERR_CUDA;
+  kernel<<<(unsigned)ctas, s.threads, bytes, st>>>(k);
+  return cuda_ok(cudaGetLastError()) ? MOE_OK : MOE_ERR_CUDA;
 }
 
 template <typename RT>
-void fwd_any(const FwdK& k, int64_t T, cudaStream_t st) {
-  const int nvec = k.d / NV;
-  auto threads = [&](int v) { return ((nvec + v - 1) / v + 31) / 32 * 32; };
-  if (nvec <= 512) fwd<RT, 1>(k, T, threads(1), st);
-  else if (nvec <= 1024) fwd<RT, 2>(k, T, threads(2), st);
-  else fwd<RT, 4>(k, T, threads(4), st);
+int fwd(const FwdK& k, int64_t ctas, cudaStream_t st) {
+  const Shape s = shape_of(k.d);
+  const int pieces = 1 + sizeof(RT) / 2;
+  static std::atomic<uint64_t> ready[4];
+  if (s.v == 1) return launch_rows(block_norm_kernel<RT, 1, 256>, ready[0], k, pieces, ctas, st);
+  if (s.v == 2 && s.threads <= 256)
+    return launch_rows(block_norm_kernel<RT, 2, 256>, ready[1], k, pieces, ctas, st);
+  if (s.v == 2) return launch_rows(block_norm_kernel<RT, 2, 512>, ready[2], k, pieces, ctas, st);
+  return launch_rows(block_norm_kernel<RT, 4, 512>, ready[3], k, pieces, ctas, st);
 }
 
 template <typename RT>
-void bwd_any(const BwdK& k, unsigned ctas, cudaStream_t st) {
-  const int nvec = k.d / NV;
-  auto threads = [&](int v) { return ((nvec + v - 1) / v + 31) / 32 * 32; };
-  if (nvec <= 512) block_norm_bwd_kernel<RT, 1><<<ctas, threads(1), 0, st>>>(k);
-  else if (nvec <= 1024) block_norm_bwd_kernel<RT, 2><<<ctas, threads(2), 0, st>>>(k);
-  else block_norm_bwd_kernel<RT, 4><<<ctas, threads(4), 0, st>>>(k);
+int bwd(const BwdK& k, int64_t ctas, cudaStream_t st) {
+  const Shape s = shape_of(k.d);
+  const int pieces = 2 + 2 * (sizeof(RT) / 2);
+  static std::atomic<uint64_t> ready[4];
+  if (s.v == 1) return launch_rows(block_norm_bwd_kernel<RT, 1, 256>, ready[0], k, pieces, ctas, st);
+  if (s.v == 2 && s.threads <= 256)
+    return launch_rows(block_norm_bwd_kernel<RT, 2, 256>, ready[1], k, pieces, ctas, st);
+  if (s.v == 2) return launch_rows(block_norm_bwd_kernel<RT, 2, 512>, ready[2], k, pieces, ctas, st);
+  return launch_rows(block_norm_bwd_kernel<RT, 4, 512>, ready[3], k, pieces, ctas, st);
 }
 
 }  // namespace
 
 size_t norm_ws_bytes(const moe_dims& dm, const moe_norm_cfg& c) {
-  return align_up((size_t)(3 * NB_CTAS + gate_rows(dm, c)) * dm.d * sizeof(float), 256);
+  int64_t rows;
+  const int64_t ctas = split_rows(dm.T, dm.d, &rows);
+  return align_up((size_t)(3 * ctas + gate_rows(dm, c)) * dm.d * sizeof(float), 256);
 }
 
 int launch_block_norm(const moe_dims& dm, const moe_norm_cfg& c, int res_type, const NormArgs& a,
@@ -370,15 +612,15 @@ int launch_block_norm(const moe_dims& dm, const moe_norm_cfg& c, int res_type, c
   k.w_pre = a.w_pre;
   k.u = a.u;
   k.n = reinterpret_cast<__nv_bfloat16*>(a.n);
-  k.seq_len = c.seq_len;
+  k.T = dm.T;
+  const int64_t ctas = split_rows(dm.T, dm.d, &k.rows);
+  k.seq_len = c.seq_len ? c.seq_len : dm.T;
   k.d = dm.d;
   k.eps = c.eps;
   k.alpha = c.res_scale;
   k.beta = c.block_scale;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (res_type == MOE_F32) fwd_any<float>(k, dm.T, st);
-  else fwd_any<__nv_bfloat16>(k, dm.T, st);
-  return cuda_ok(cudaGetLastError()) ? MOE_OK : MOE_ERR_CUDA;
+  return res_type == MOE_F32 ? fwd<float>(k, ctas, st) : fwd<__nv_bfloat16>(k, ctas, st);
 }
 
 int launch_block_norm_bwd(const moe_dims& dm, const moe_norm_cfg& c, int res_type,
@@ -397,21 +639,20 @@ int launch_block_norm_bwd(const moe_dims& dm, const moe_norm_cfg& c, int res_typ
   k.dy = reinterpret_cast<__nv_bfloat16*>(a.dy);
   k.dres = a.dres;
   float* ws = reinterpret_cast<float*>(a.ws);
+  const int64_t ctas = split_rows(dm.T, dm.d, &k.rows);
   k.post = a.dw_post ? ws : nullptr;
-  k.pre = a.dw_pre ? ws + (size_t)NB_CTAS * dm.d : nullptr;
-  k.seq = a.dgate ? ws + (size_t)2 * NB_CTAS * dm.d : nullptr;
+  k.pre = a.dw_pre ? ws + (size_t)ctas * dm.d : nullptr;
+  k.seq = a.dgate ? ws + (size_t)2 * ctas * dm.d : nullptr;
   k.T = dm.T;
-  k.rows = (dm.T + NB_CTAS - 1) / NB_CTAS;
   k.seq_len = c.seq_len ? c.seq_len : (dm.T ? dm.T : 1);
   k.d = dm.d;
   k.eps = c.eps;
   k.alpha = c.res_scale;
   k.beta = c.block_scale;
-  const unsigned ctas = dm.T ? (unsigned)((dm.T + k.rows - 1) / k.rows) : 0;
   if (ctas) {
-    if (res_type == MOE_F32) bwd_any<float>(k, ctas, st);
-    else bwd_any<__nv_bfloat16>(k, ctas, st);
-    if (!cuda_ok(cudaGetLastError())) return MOE_ERR_CUDA;
+    const int rc =
+        res_type == MOE_F32 ? bwd<float>(k, ctas, st) : bwd<__nv_bfloat16>(k, ctas, st);
+    if (rc != MOE_OK) return rc;
   }
   if (!a.dw_post && !a.dw_pre && !a.dgate) return MOE_OK;
   FinK f{};
@@ -423,7 +664,7 @@ int launch_block_norm_bwd(const moe_dims& dm, const moe_norm_cfg& c, int res_typ
   f.dw_pre = a.dw_pre;
   f.dgate = a.dgate;
   f.T = dm.T;
-  f.rows = k.rows ? k.rows : 1;
+  f.rows = k.rows;
   f.seq_len = k.seq_len;
   f.ctas = (int)ctas;
   f.d = dm.d;
