@@ -45,60 +45,129 @@ Shape shape_of(int d) {
   return s;
 }
 
+// Two FP32 values in a register pair, for the paired FP32 instructions (each half rounds
+// like the single instruction).
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 halves(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float v) { return pair(v, v); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum2(f32x2 v) {
+  const float2 f = halves(v);
+  return f.x + f.y;
+}
+
+// Eight columns.
 struct F8 {
-  float v[NV];
+  f32x2 v[NV / 2];
 };
 
-__device__ __forceinline__ F8 ld8(const __nv_bfloat16* p) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ F8 splat(float f) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < NV / 2; ++i) r.v[i] = both(f);
+  return r;
+}
+__device__ __forceinline__ F8 from_bf16(const uint4& u) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   F8 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = __uint_as_float(w[i] << 16);
-    r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    r.v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   return r;
 }
 __device__ __forceinline__ F8 ld8(const float* p) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+  return F8{{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
 }
 __device__ __forceinline__ void st8(__nv_bfloat16* p, const F8& r) {
   uint4 u;
   uint32_t* w = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(r.v[2 * i], r.v[2 * i + 1]);
+    const __nv_bfloat162 b = __float22bfloat162_rn(halves(r.v[i]));
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
   *reinterpret_cast<uint4*>(p) = u;
 }
 __device__ __forceinline__ void st8(float* p, const F8& r) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+  const float2 a = halves(r.v[0]), b = halves(r.v[1]), c = halves(r.v[2]), d = halves(r.v[3]);
+  reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
 }
 
-// Sums of N values over the CTA, the same bits in every thread.  Calls alternate between
-// two halves of sh [2][16][N], so one barrier a call is enough.
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float* sh, int& half) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  float* mine = sh + half * 16 * N;
+constexpr int MAX_WARPS = 16;  // of a CTA
+
+// Sum over the CTA, the same bits in every thread.  Calls alternate between two halves of
+// sh [2][MAX_WARPS] (zero beyond the CTA's warps), so one barrier a call is enough.
+__device__ __forceinline__ float block_sum1(float v, float* sh, int& half) {
+  float* mine = sh + half * MAX_WARPS;
   half ^= 1;
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (lane == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) mine[warp * N + i] = v[i];
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = v;
   __syncthreads();
+  float s = 0.0f;
+  const int quads = (int)(blockDim.x + 127) >> 7;
+  for (int i = 0; i < quads; ++i) {
+    const float4 f = reinterpret_cast<const float4*>(mine)[i];
+    s += (f.x + f.y) + (f.z + f.w);
+  }
+  return s;
+}
+
+// Six sums over the CTA.  In a warp the lanes halve the values they carry at every step
+// (3 + 2 + 1 + 1 + 1 shuffles where six sums take 30): lanes 4 i .. 4 i + 3 end with value
+// i (values 3 and 7 are not used).  sh [2][MAX_WARPS][8] as above; every warp then adds the
+// warps' rows and hands all six to every lane.
+__device__ __forceinline__ void block_sum6(float (&v)[6], float* sh, int& half) {
+  constexpr unsigned ALL = 0xffffffffu;
+  float* mine = sh + half * MAX_WARPS * 8;
+  half ^= 1;
+  const int lane = threadIdx.x & 31;
+  const bool up16 = lane & 16, up8 = lane & 8, up4 = lane & 4;
+  float w[4];
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = mine[i];
-  for (int w = 1; w < nw; ++w)
+  for (int i = 0; i < 3; ++i) {
+    const float keep = up16 ? v[3 + i] : v[i], give = up16 ? v[i] : v[3 + i];
+    w[i] = keep + __shfl_xor_sync(ALL, give, 16);
+  }
+  w[3] = 0.0f;
+  float x[2];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += mine[w * N + i];
+  for (int i = 0; i < 2; ++i) {
+    const float keep = up8 ? w[2 + i] : w[i], give = up8 ? w[i] : w[2 + i];
+    x[i] = keep + __shfl_xor_sync(ALL, give, 8);
+  }
+  float y = (up4 ? x[1] : x[0]) + __shfl_xor_sync(ALL, up4 ? x[0] : x[1], 4);
+  y += __shfl_xor_sync(ALL, y, 2);
+  y += __shfl_xor_sync(ALL, y, 1);
+  if ((lane & 3) == 0) mine[(threadIdx.x >> 5) * 8 + (lane >> 2)] = y;
+  __syncthreads();
+  // lane l adds value l / 4 of warps l % 4, l % 4 + 4, ...
+  float s = 0.0f;
+  for (int r = lane & 3; r < (int)(blockDim.x >> 5); r += 4) s += mine[r * 8 + (lane >> 2)];
+  s += __shfl_xor_sync(ALL, s, 2);
+  s += __shfl_xor_sync(ALL, s, 1);
+#pragma unroll
+  for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(ALL, s, 4 * (i < 3 ? i : i + 1));
 }
 
 __device__ __forceinline__ void cp16(uint4* dst, const void* src) {
@@ -129,12 +198,12 @@ __device__ __forceinline__ void cp_row(uint4* st, int nvec, int c, const float* 
   cp16(st + nvec + c, g + 4);
 }
 __device__ __forceinline__ F8 rd_row(const uint4* st, int nvec, int c, const __nv_bfloat16*) {
-  return ld8(reinterpret_cast<const __nv_bfloat16*>(st + c));
+  return from_bf16(st[c]);
 }
 __device__ __forceinline__ F8 rd_row(const uint4* st, int nvec, int c, const float*) {
   const float4 a = *reinterpret_cast<const float4*>(st + c);
   const float4 b = *reinterpret_cast<const float4*>(st + nvec + c);
-  return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+  return F8{{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
 }
 
 struct FwdK {
@@ -151,57 +220,65 @@ struct FwdK {
 // beta gate w_post of a vector (w_post and gate may be NULL).
 __device__ __forceinline__ F8 post_factor(const float* w_post, const float* gate, float beta,
                                           int c) {
-  F8 f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) f.v[j] = beta;
+  F8 f = splat(beta);
   if (w_post) {
     const F8 w = ld8(w_post + c * NV);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) f.v[j] *= w.v[j];
+    for (int j = 0; j < NV / 2; ++j) f.v[j] = mul2(f.v[j], w.v[j]);
   }
   if (gate) {
     const F8 g = ld8(gate + c * NV);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) f.v[j] *= g.v[j];
+    for (int j = 0; j < NV / 2; ++j) f.v[j] = mul2(f.v[j], g.v[j]);
   }
   return f;
 }
 
-template <typename RT, int V, int THREADS>
+// FULL: every thread has V vectors of the row.
+template <typename RT, int V, int THREADS, bool FULL>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(const FwdK a) {
   constexpr bool KEEP = V <= 2;  // the weights in registers; else read again every row
-  constexpr int R = sizeof(RT) / 2;
+  constexpr int R = sizeof(RT) / 2, H = NV / 2;
   extern __shared__ uint4 ring[];
-  __shared__ float sh[2 * 16];
+  __shared__ __align__(16) float sh[2 * MAX_WARPS];
   int half = 0;
   const int nvec = a.d / NV, tid = threadIdx.x, nt = blockDim.x;
   const int64_t t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
   const int S = a.stages, row_v = (1 + R) * nvec;  // a stage: y, then res
-  const RT* res = reinterpret_cast<const RT*>(a.res);
-  RT* u_out = reinterpret_cast<RT*>(a.u);
-  int put = 0, get = 0;  // ring stages of the next row to copy and to read
-  auto issue = [&](int64_t t) {
-    if (t < t1) {
-      uint4* st = ring + (size_t)put * row_v;
-      put = put + 1 == S ? 0 : put + 1;
+  if (tid < 2 * MAX_WARPS) sh[tid] = 0.0f;
+  __syncthreads();
+  auto on = [&](int i) { return FULL || tid + i * nt < nvec; };
+  // this thread's first vector of the next row to copy, and of the row being worked on
+  const __nv_bfloat16* y_next = a.y + t0 * a.d + tid * NV;
+  const RT* res_next = reinterpret_cast<const RT*>(a.res) + t0 * a.d + tid * NV;
+  RT* u_out = reinterpret_cast<RT*>(a.u) + t0 * a.d + tid * NV;
+  __nv_bfloat16* n_out = a.n + t0 * a.d + tid * NV;
+  int put = 0, get = 0;  // ring stages of those rows
+  int left = (int)(t1 - t0);
+  auto issue = [&]() {
+    if (left > 0) {
+      uint4* st = ring + put * row_v;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = tid + i * nt;
-        if (c >= nvec) continue;
-        const int64_t at = t * a.d + c * NV;
-        if (a.y) cp_row(st, nvec, c, a.y + at);
-        cp_row(st + nvec, nvec, c, res + at);
-      }
+      for (int i = 0; i < V; ++i)
+        if (on(i)) {
+          if (a.y) cp_row(st, nvec, tid + i * nt, y_next + i * nt * NV);
+          cp_row(st + nvec, nvec, tid + i * nt, res_next + i * nt * NV);
+        }
+      y_next += a.d;
+      res_next += a.d;
+      --left;
+      put = put + 1 == S ? 0 : put + 1;
     }
     cp_commit();
   };
-  for (int s = 0; s + 1 < S; ++s) issue(t0 + s);
+  for (int s = 0; s + 1 < S; ++s) issue();
   F8 f[KEEP ? V : 1], wp[KEEP ? V : 1];
   if constexpr (KEEP) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (a.w_pre && tid + i * nt < nvec) wp[i] = ld8(a.w_pre + (tid + i * nt) * NV);
+      if (a.w_pre && on(i)) wp[i] = ld8(a.w_pre + (tid + i * nt) * NV);
   }
+  const float inv_d = 1.0f / a.d;
   int64_t seq_end = t0;  // first token past the gate row that f holds
   const float* gate = nullptr;
   for (int64_t t = t0; t < t1; ++t) {
@@ -212,75 +289,72 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(cons
       if constexpr (KEEP) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (a.y && tid + i * nt < nvec)
-            f[i] = post_factor(a.w_post, gate, a.beta, tid + i * nt);
+          if (a.y && on(i)) f[i] = post_factor(a.w_post, gate, a.beta, tid + i * nt);
       }
     }
     if (S == 1) {
       __syncthreads();
-      issue(t);
+      issue();
     }
     cp_wait(S > 1 ? S - 2 : 0);
-    const uint4* st = ring + (size_t)get * row_v;
+    const uint4* st = ring + get * row_v;
     get = get + 1 == S ? 0 : get + 1;
     F8 u[V];
-    float s[1] = {0.0f};
+    f32x2 s = both(0.0f);
     if (a.y) {
       F8 y[V];
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (tid + i * nt < nvec) {
+        if (on(i)) {
           y[i] = rd_row(st, nvec, tid + i * nt, a.y);
 #pragma unroll
-          for (int j = 0; j < NV; ++j) s[0] = fmaf(y[i].v[j], y[i].v[j], s[0]);
+          for (int j = 0; j < H; ++j) s = fma2(y[i].v[j], y[i].v[j], s);
         }
       float r1 = 1.0f;
-      if (a.w_post) {
-        block_sum<1>(s, sh, half);
-        r1 = rsqrtf(s[0] / a.d + a.eps);
-      }
-      s[0] = 0.0f;
+      if (a.w_post) r1 = rsqrtf(fmaf(block_sum1(sum2(s), sh, half), inv_d, a.eps));
+      const f32x2 rr = both(r1), al = both(a.alpha);
+      s = both(0.0f);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = tid + i * nt;
-        if (c >= nvec) continue;
-        u[i] = rd_row(st + nvec, nvec, c, res);
-        const F8 g = KEEP ? f[KEEP ? i : 0] : post_factor(a.w_post, gate, a.beta, c);
+      for (int i = 0; i < V; ++i)
+        if (on(i)) {
+          u[i] = rd_row(st + nvec, nvec, tid + i * nt, reinterpret_cast<const RT*>(a.res));
+          const F8 g = KEEP ? f[KEEP ? i : 0] : post_factor(a.w_post, gate, a.beta, tid + i * nt);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          u[i].v[j] = fmaf(g.v[j] * r1, y[i].v[j], a.alpha * u[i].v[j]);
-          s[0] = fmaf(u[i].v[j], u[i].v[j], s[0]);
+          for (int j = 0; j < H; ++j) {
+            u[i].v[j] = fma2(al, u[i].v[j], mul2(mul2(g.v[j], rr), y[i].v[j]));
+            s = fma2(u[i].v[j], u[i].v[j], s);
+          }
+          st8(u_out + i * nt * NV, u[i]);
         }
-        st8(u_out + t * a.d + c * NV, u[i]);
-      }
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (tid + i * nt < nvec) {
-          u[i] = rd_row(st + nvec, nvec, tid + i * nt, res);
+        if (on(i)) {
+          u[i] = rd_row(st + nvec, nvec, tid + i * nt, reinterpret_cast<const RT*>(a.res));
 #pragma unroll
-          for (int j = 0; j < NV; ++j) s[0] = fmaf(u[i].v[j], u[i].v[j], s[0]);
+          for (int j = 0; j < H; ++j) s = fma2(u[i].v[j], u[i].v[j], s);
         }
     }
     // a copy refills the stage of the row before this one: every thread has passed a
     // barrier since it read that
     if (a.n) {
-      block_sum<1>(s, sh, half);
-      if (S > 1) issue(t + S - 1);
-      const float r2 = rsqrtf(s[0] / a.d + a.eps);
+      const float ss = block_sum1(sum2(s), sh, half);
+      if (S > 1) issue();
+      const f32x2 r2 = both(rsqrtf(fmaf(ss, inv_d, a.eps)));
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = tid + i * nt;
-        if (c >= nvec) continue;
-        F8 w = KEEP ? wp[KEEP ? i : 0] : ld8(a.w_pre + c * NV);
+      for (int i = 0; i < V; ++i)
+        if (on(i)) {
+          F8 w = KEEP ? wp[KEEP ? i : 0] : ld8(a.w_pre + (tid + i * nt) * NV);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) w.v[j] *= u[i].v[j] * r2;
-        st8(a.n + t * a.d + c * NV, w);
-      }
+          for (int j = 0; j < H; ++j) w.v[j] = mul2(mul2(w.v[j], r2), u[i].v[j]);
+          st8(n_out + i * nt * NV, w);
+        }
     } else {
       if (!a.w_post) __syncthreads();  // as a statistic's barrier
-      if (S > 1) issue(t + S - 1);
+      if (S > 1) issue();
     }
+    u_out += a.d;
+    n_out += a.d;
   }
 }
 
@@ -303,71 +377,77 @@ struct BwdK {
   float eps, alpha, beta;
 };
 
-template <typename RT, int V, int THREADS>
+template <typename RT, int V, int THREADS, bool FULL>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(const BwdK a) {
   constexpr bool KEEP = V <= 2;
-  constexpr int R = sizeof(RT) / 2;
+  constexpr int R = sizeof(RT) / 2, H = NV / 2;
   extern __shared__ uint4 ring[];
-  __shared__ float sh[2 * 16 * 6];
+  __shared__ float sh[2 * MAX_WARPS * 8];
   int half = 0;
   const int nvec = a.d / NV, tid = threadIdx.x, nt = blockDim.x;
   const int64_t t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
   const int S = a.stages, row_v = (2 + 2 * R) * nvec;  // a stage: dn, y, dres_out, u
-  const RT* du_in = reinterpret_cast<const RT*>(a.du);
-  const RT* u_in = reinterpret_cast<const RT*>(a.u);
-  RT* dres_out = reinterpret_cast<RT*>(a.dres);
-  int put = 0, get = 0;  // ring stages of the next row to copy and to read
-  auto issue = [&](int64_t t) {
-    if (t < t1) {
-      uint4* st = ring + (size_t)put * row_v;
-      put = put + 1 == S ? 0 : put + 1;
+  auto on = [&](int i) { return FULL || tid + i * nt < nvec; };
+  // this thread's first vector of the next row to copy, and of the row being worked on
+  const int64_t first = t0 * a.d + tid * NV;
+  const __nv_bfloat16 *dn_next = a.dn + first, *y_next = a.y + first;
+  const RT* du_next = reinterpret_cast<const RT*>(a.du) + first;
+  const RT* u_next = reinterpret_cast<const RT*>(a.u) + first;
+  RT* dres_out = reinterpret_cast<RT*>(a.dres) + first;
+  __nv_bfloat16* dy_out = a.dy + first;
+  int put = 0, get = 0;
+  int left = (int)(t1 - t0);
+  auto issue = [&]() {
+    if (left > 0) {
+      uint4* st = ring + put * row_v;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = tid + i * nt;
-        if (c >= nvec) continue;
-        const int64_t at = t * a.d + c * NV;
-        if (a.dn) {
-          cp_row(st, nvec, c, a.dn + at);
-          cp_row(st + (2 + R) * nvec, nvec, c, u_in + at);
+      for (int i = 0; i < V; ++i)
+        if (on(i)) {
+          const int c = tid + i * nt, o = i * nt * NV;
+          if (a.dn) {
+            cp_row(st, nvec, c, dn_next + o);
+            cp_row(st + (2 + R) * nvec, nvec, c, u_next + o);
+          }
+          if (a.y) cp_row(st + nvec, nvec, c, y_next + o);
+          if (a.du) cp_row(st + 2 * nvec, nvec, c, du_next + o);
         }
-        if (a.y) cp_row(st + nvec, nvec, c, a.y + at);
-        if (a.du) cp_row(st + 2 * nvec, nvec, c, du_in + at);
-      }
+      dn_next += a.d;
+      y_next += a.d;
+      du_next += a.d;
+      u_next += a.d;
+      --left;
+      put = put + 1 == S ? 0 : put + 1;
     }
     cp_commit();
   };
   // matrices that are not there read as zeros: no copy ever writes their part of the ring
-  for (int s = 0; s < S; ++s)
+  if (!a.dn || !a.y || !a.du)
+    for (int s = 0; s < S; ++s)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = tid + i * nt;
-      if (c >= nvec) continue;
-      uint4* st = ring + (size_t)s * row_v;
-      const uint4 z = make_uint4(0, 0, 0, 0);
-      if (!a.dn) {
-        st[c] = z;
+      for (int i = 0; i < V; ++i)
+        if (on(i)) {
+          uint4* st = ring + s * row_v + tid + i * nt;
+          const uint4 z = make_uint4(0, 0, 0, 0);
+          if (!a.dn) st[0] = z;
+          if (!a.y) st[nvec] = z;
 #pragma unroll
-        for (int r = 0; r < R; ++r) st[(2 + R + r) * nvec + c] = z;
-      }
-      if (!a.y) st[nvec + c] = z;
-      if (!a.du) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) st[(2 + r) * nvec + c] = z;
-      }
-    }
-  for (int s = 0; s + 1 < S; ++s) issue(t0 + s);
+          for (int r = 0; r < R; ++r) {
+            if (!a.du) st[(2 + r) * nvec] = z;
+            if (!a.dn) st[(2 + R + r) * nvec] = z;
+          }
+        }
+  for (int s = 0; s + 1 < S; ++s) issue();
   F8 sa[V], sb[V], f[KEEP ? V : 1], wp[KEEP ? V : 1];
+  const F8 zero = splat(0.0f);
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int j = 0; j < NV; ++j) sa[i].v[j] = sb[i].v[j] = 0.0f;
-  const F8 zero = sa[0];
+  for (int i = 0; i < V; ++i) sa[i] = sb[i] = zero;
   if constexpr (KEEP) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      wp[i] = a.dn && tid + i * nt < nvec ? ld8(a.w_pre + (tid + i * nt) * NV) : zero;
+      wp[i] = a.dn && on(i) ? ld8(a.w_pre + (tid + i * nt) * NV) : zero;
   }
-  const float inv_d = 1.0f / a.d, alpha = a.y ? a.alpha : 1.0f;
+  const float inv_d = 1.0f / a.d;
+  const f32x2 alpha = both(a.y ? a.alpha : 1.0f);
   int64_t seq_end = t0, seq = 0;  // the gate row that f holds, and the first token past it
   const float* gate = nullptr;
   bool flushed = false;  // post holds the sums of earlier gate rows
@@ -379,103 +459,109 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
       if constexpr (KEEP) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          f[i] = a.y && tid + i * nt < nvec ? post_factor(a.w_post, gate, a.beta, tid + i * nt)
-                                            : zero;
+          f[i] = a.y && on(i) ? post_factor(a.w_post, gate, a.beta, tid + i * nt) : zero;
       }
     }
     if (S == 1) {
       __syncthreads();
-      issue(t);
+      issue();
     }
     cp_wait(S > 1 ? S - 2 : 0);
-    const uint4* st = ring + (size_t)get * row_v;
+    const uint4* st = ring + get * row_v;
     get = get + 1 == S ? 0 : get + 1;
-    float sum[6] = {0, 0, 0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
+    F8 dn[V], y[V], du[V], u[V];
+    auto read = [&](int i) {
       const int c = tid + i * nt;
-      if (c >= nvec) continue;
-      const F8 dn = rd_row(st, nvec, c, a.dn), y = rd_row(st + nvec, nvec, c, a.y);
-      const F8 du = rd_row(st + 2 * nvec, nvec, c, du_in);
-      const F8 u = rd_row(st + (2 + R) * nvec, nvec, c, u_in);
-      F8 g, w;
+      dn[i] = rd_row(st, nvec, c, a.dn);
+      y[i] = rd_row(st + nvec, nvec, c, a.y);
+      du[i] = rd_row(st + 2 * nvec, nvec, c, reinterpret_cast<const RT*>(a.du));
+      u[i] = rd_row(st + (2 + R) * nvec, nvec, c, reinterpret_cast<const RT*>(a.u));
+    };
+    auto factors = [&](int i, F8& g, F8& w) {
       if constexpr (KEEP) {
         g = f[i];
         w = wp[i];
       } else {
-        g = a.y ? post_factor(a.w_post, gate, a.beta, c) : zero;
-        w = a.dn ? ld8(a.w_pre + c * NV) : zero;
+        g = a.y ? post_factor(a.w_post, gate, a.beta, tid + i * nt) : zero;
+        w = a.dn ? ld8(a.w_pre + (tid + i * nt) * NV) : zero;
       }
+    };
+    f32x2 s[6];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const float an = dn.v[j] * w.v[j], qy = g.v[j] * y.v[j];
-        sum[0] = fmaf(u.v[j], u.v[j], sum[0]);
-        sum[1] = fmaf(an, u.v[j], sum[1]);
-        sum[2] = fmaf(y.v[j], y.v[j], sum[2]);
-        sum[3] = fmaf(qy, du.v[j], sum[3]);
-        sum[4] = fmaf(qy, an, sum[4]);
-        sum[5] = fmaf(qy, u.v[j], sum[5]);
+    for (int j = 0; j < 6; ++j) s[j] = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (on(i)) {
+        read(i);
+        F8 g, w;
+        factors(i, g, w);
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          const f32x2 an = mul2(dn[i].v[j], w.v[j]), qy = mul2(g.v[j], y[i].v[j]);
+          s[0] = fma2(u[i].v[j], u[i].v[j], s[0]);
+          s[1] = fma2(an, u[i].v[j], s[1]);
+          s[2] = fma2(y[i].v[j], y[i].v[j], s[2]);
+          s[3] = fma2(qy, du[i].v[j], s[3]);
+          s[4] = fma2(qy, an, s[4]);
+          s[5] = fma2(qy, u[i].v[j], s[5]);
+        }
       }
-    }
-    block_sum<6>(sum, sh, half);
+    float sum[6];
+#pragma unroll
+    for (int j = 0; j < 6; ++j) sum[j] = sum2(s[j]);
+    block_sum6(sum, sh, half);
     // the stage of the row before this one: every thread has passed a barrier since it read it
-    if (S > 1) issue(t + S - 1);
+    if (S > 1) issue();
     const float r2 = a.dn ? rsqrtf(fmaf(sum[0], inv_d, a.eps)) : 0.0f;
     const float c2 = r2 * r2 * r2 * sum[1] * inv_d;
     const float r1 = a.w_post ? rsqrtf(fmaf(sum[2], inv_d, a.eps)) : 1.0f;
     const float c1 =
         a.w_post ? r1 * r1 * r1 * inv_d * (sum[3] + r2 * sum[4] - c2 * sum[5]) : 0.0f;
+    const f32x2 r1p = both(r1), r2p = both(r2), c1n = both(-c1), c2n = both(-c2);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = tid + i * nt;
-      if (c >= nvec) continue;
-      const F8 dn = rd_row(st, nvec, c, a.dn), y = rd_row(st + nvec, nvec, c, a.y);
-      const F8 du = rd_row(st + 2 * nvec, nvec, c, du_in);
-      const F8 u = rd_row(st + (2 + R) * nvec, nvec, c, u_in);
-      F8 g, w, dres, dy;
-      if constexpr (KEEP) {
-        g = f[i];
-        w = wp[i];
-      } else {
-        g = a.y ? post_factor(a.w_post, gate, a.beta, c) : zero;
-        w = a.dn ? ld8(a.w_pre + c * NV) : zero;
-      }
+    for (int i = 0; i < V; ++i)
+      if (on(i)) {
+        read(i);
+        F8 g, w, dres, dy;
+        factors(i, g, w);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const float v = du.v[j] + (r2 * (dn.v[j] * w.v[j]) - c2 * u.v[j]);
-        dres.v[j] = alpha * v;
-        const float x = r1 * v;
-        dy.v[j] = g.v[j] * x - c1 * y.v[j];
-        sa[i].v[j] = fmaf(x, y.v[j], sa[i].v[j]);
-        sb[i].v[j] = fmaf(dn.v[j], r2 * u.v[j], sb[i].v[j]);
+        for (int j = 0; j < H; ++j) {
+          const f32x2 dr = mul2(dn[i].v[j], r2p);  // dn / rms(u)
+          const f32x2 v = fma2(dr, w.v[j], fma2(c2n, u[i].v[j], du[i].v[j]));
+          dres.v[j] = mul2(alpha, v);
+          const f32x2 x = mul2(r1p, v);
+          dy.v[j] = fma2(g.v[j], x, mul2(c1n, y[i].v[j]));
+          sa[i].v[j] = fma2(x, y[i].v[j], sa[i].v[j]);
+          sb[i].v[j] = fma2(dr, u[i].v[j], sb[i].v[j]);
+        }
+        st8(dres_out + i * nt * NV, dres);
+        if (a.y) st8(dy_out + i * nt * NV, dy);
       }
-      const int64_t at = t * a.d + c * NV;
-      st8(dres_out + at, dres);
-      if (a.y) st8(a.dy + at, dy);
-    }
+    dres_out += a.d;
+    dy_out += a.d;
     if (t + 1 == t1 || t + 1 == seq_end) {  // the gate row's sums are complete here
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = tid + i * nt;
-        if (c >= nvec) continue;
-        if (a.seq) st8(a.seq + ((int64_t)blockIdx.x + seq) * a.d + c * NV, sa[i]);
-        if (a.post) {
-          float* p = a.post + (int64_t)blockIdx.x * a.d + c * NV;
-          F8 v = flushed ? ld8(p) : zero;
-          const F8 g = gate ? ld8(gate + c * NV) : zero;
+      for (int i = 0; i < V; ++i)
+        if (on(i)) {
+          const int c = tid + i * nt;
+          if (a.seq) st8(a.seq + ((int64_t)blockIdx.x + seq) * a.d + c * NV, sa[i]);
+          if (a.post) {
+            float* p = a.post + (int64_t)blockIdx.x * a.d + c * NV;
+            F8 v = flushed ? ld8(p) : zero;
+            const F8 g = gate ? ld8(gate + c * NV) : splat(1.0f);
 #pragma unroll
-          for (int j = 0; j < NV; ++j) v.v[j] += gate ? g.v[j] * sa[i].v[j] : sa[i].v[j];
-          st8(p, v);
+            for (int j = 0; j < H; ++j) v.v[j] = fma2(g.v[j], sa[i].v[j], v.v[j]);
+            st8(p, v);
+          }
+          sa[i] = zero;
         }
-        sa[i] = zero;
-      }
       flushed = true;
     }
   }
   if (a.pre)
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (tid + i * nt < nvec) st8(a.pre + (int64_t)blockIdx.x * a.d + (tid + i * nt) * NV, sb[i]);
+      if (on(i)) st8(a.pre + (int64_t)blockIdx.x * a.d + (tid + i * nt) * NV, sb[i]);
 }
 
 struct FinK {
@@ -571,26 +657,38 @@ int launch_rows(void (*kernel)(const K), std::atomic<uint64_t>& ready, K k, int 
 
 template <typename RT>
 int fwd(const FwdK& k, int64_t ctas, cudaStream_t st) {
+  static std::atomic<uint64_t> ready[7];
   const Shape s = shape_of(k.d);
-  const int pieces = 1 + sizeof(RT) / 2;
-  static std::atomic<uint64_t> ready[4];
-  if (s.v == 1) return launch_rows(block_norm_kernel<RT, 1, 256>, ready[0], k, pieces, ctas, st);
+  const int p = 1 + sizeof(RT) / 2;
+  const bool full = s.v * s.threads == k.d / NV;
+  if (s.v == 1)
+    return full ? launch_rows(block_norm_kernel<RT, 1, 256, true>, ready[0], k, p, ctas, st)
+                : launch_rows(block_norm_kernel<RT, 1, 256, false>, ready[1], k, p, ctas, st);
   if (s.v == 2 && s.threads <= 256)
-    return launch_rows(block_norm_kernel<RT, 2, 256>, ready[1], k, pieces, ctas, st);
-  if (s.v == 2) return launch_rows(block_norm_kernel<RT, 2, 512>, ready[2], k, pieces, ctas, st);
-  return launch_rows(block_norm_kernel<RT, 4, 512>, ready[3], k, pieces, ctas, st);
+    return full ? launch_rows(block_norm_kernel<RT, 2, 256, true>, ready[2], k, p, ctas, st)
+                : launch_rows(block_norm_kernel<RT, 2, 256, false>, ready[3], k, p, ctas, st);
+  if (s.v == 2)
+    return full ? launch_rows(block_norm_kernel<RT, 2, 512, true>, ready[4], k, p, ctas, st)
+                : launch_rows(block_norm_kernel<RT, 2, 512, false>, ready[5], k, p, ctas, st);
+  return launch_rows(block_norm_kernel<RT, 4, 512, false>, ready[6], k, p, ctas, st);
 }
 
 template <typename RT>
 int bwd(const BwdK& k, int64_t ctas, cudaStream_t st) {
+  static std::atomic<uint64_t> ready[7];
   const Shape s = shape_of(k.d);
-  const int pieces = 2 + 2 * (sizeof(RT) / 2);
-  static std::atomic<uint64_t> ready[4];
-  if (s.v == 1) return launch_rows(block_norm_bwd_kernel<RT, 1, 256>, ready[0], k, pieces, ctas, st);
+  const int p = 2 + 2 * (sizeof(RT) / 2);
+  const bool full = s.v * s.threads == k.d / NV;
+  if (s.v == 1)
+    return full ? launch_rows(block_norm_bwd_kernel<RT, 1, 256, true>, ready[0], k, p, ctas, st)
+                : launch_rows(block_norm_bwd_kernel<RT, 1, 256, false>, ready[1], k, p, ctas, st);
   if (s.v == 2 && s.threads <= 256)
-    return launch_rows(block_norm_bwd_kernel<RT, 2, 256>, ready[1], k, pieces, ctas, st);
-  if (s.v == 2) return launch_rows(block_norm_bwd_kernel<RT, 2, 512>, ready[2], k, pieces, ctas, st);
-  return launch_rows(block_norm_bwd_kernel<RT, 4, 512>, ready[3], k, pieces, ctas, st);
+    return full ? launch_rows(block_norm_bwd_kernel<RT, 2, 256, true>, ready[2], k, p, ctas, st)
+                : launch_rows(block_norm_bwd_kernel<RT, 2, 256, false>, ready[3], k, p, ctas, st);
+  if (s.v == 2)
+    return full ? launch_rows(block_norm_bwd_kernel<RT, 2, 512, true>, ready[4], k, p, ctas, st)
+                : launch_rows(block_norm_bwd_kernel<RT, 2, 512, false>, ready[5], k, p, ctas, st);
+  return launch_rows(block_norm_bwd_kernel<RT, 4, 512, false>, ready[6], k, p, ctas, st);
 }
 
 }  // namespace
