@@ -395,22 +395,31 @@ def _types():
         _TYPES.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16})
         _TYPES.update(f32=torch.float32, i32=torch.int32, bf16=torch.bfloat16, u8=torch.uint8,
                       f64=torch.float64, device=torch.cuda.current_device)
+        # the same numbers without a Stream object and the lazy start of CUDA on the way
+        # (1.5 us less a call); a torch without the call keeps to the public ones
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _TYPES["stream"] = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
     return _TYPES
+
+
+def _here(stream, dev):
+    """As _s, on the current device ``dev``."""
+    return _types()["stream"](dev) if stream is None else _s(stream)
 
 
 def _need(what, t, dtype, numel, dev):
     """Device pointer of a tensor after its checks; NULL for None."""
     if t is None or type(t) is int:
         return t
+    if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{what}: {t.dtype} given, {dtype} needed")
     if t.numel() != numel:
         raise ValueError(f"{what}: shape {tuple(t.shape)} has {t.numel()} elements, {numel} needed")
     if not t.is_contiguous():
         raise ValueError(f"{what}: not contiguous (strides {t.stride()})")
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: on {t.device}, the current device is cuda:{dev}")
-    return t.data_ptr()
+    raise ValueError(f"{what}: on {t.device}, the current device is cuda:{dev}")
 
 
 def _kind(what, t, allowed):
@@ -434,7 +443,7 @@ def moe_gate_logits(dims, x, wg, logits, ws, stream=None):
     _ck(load().moe_gate_logits(ctypes.byref(dims), _need("x", x, y["bf16"], T * d, dev),
                                _need("wg", wg, y["f32"], E * d, dev),
                                _need("logits", logits, y["f32"], T * E, dev),
-                               *_bytes("ws", ws, dev), _s(stream)), "moe_gate_logits")
+                               *_bytes("ws", ws, dev), _here(stream, dev)), "moe_gate_logits")
 
 
 def moe_route_topk(dims, cfg, logits, bias, topk_idx, topk_w, probs, stream=None):
@@ -447,7 +456,7 @@ def moe_route_topk(dims, cfg, logits, bias, topk_idx, topk_w, probs, stream=None
                               _need("bias", bias, f32, E, dev),
                               _need("topk_idx", topk_idx, y["i32"], T * k, dev),
                               _need("topk_w", topk_w, f32, T * k, dev),
-                              _need("probs", probs, f32, T * E, dev), _s(stream)),
+                              _need("probs", probs, f32, T * E, dev), _here(stream, dev)),
         "moe_route_topk")
 
 
@@ -467,7 +476,8 @@ def moe_route_bwd(dims, cfg, logits, topk_idx, topk_w, dw, seq_grad, seq_len, dl
                              _need("topk_w", topk_w, f32, T * k, dev),
                              _need("dw", dw, f32, T * k, dev),
                              _need("seq_grad", seq_grad, f32, rows * E, dev), seq_len,
-                             _need("dlogits", dlogits, logits.dtype, T * E, dev), _s(stream)),
+                             _need("dlogits", dlogits, logits.dtype, T * E, dev),
+                             _here(stream, dev)),
         "moe_route_bwd")
 
 
@@ -480,7 +490,7 @@ def moe_gate_bwd(dims, x, wg, dlogits, dx, dwg, accumulate, ws, stream=None):
                             _need("dlogits", dlogits, f32, T * E, dev),
                             _need("dx", dx, y["bf16"], T * d, dev),
                             _need("dwg", dwg, f32, E * d, dev), int(accumulate),
-                            *_bytes("ws", ws, dev), _s(stream)), "moe_gate_bwd")
+                            *_bytes("ws", ws, dev), _here(stream, dev)), "moe_gate_bwd")
 
 
 # ------------------------------------------------------------- block norms --
@@ -499,7 +509,7 @@ def moe_block_norm(dims, cfg, y, res, w_post, gate, w_pre, res_out, n, stream=No
                               _need("gate", gate, f32, _gate_rows(dims, cfg) * d, dev),
                               _need("w_pre", w_pre, f32, d, dev),
                               _need("res_out", res_out, res.dtype, m, dev),
-                              _need("n", n, bf, m, dev), _s(stream)), "moe_block_norm")
+                              _need("n", n, bf, m, dev), _here(stream, dev)), "moe_block_norm")
 
 
 def moe_norm_workspace_size(dims, cfg) -> int:
@@ -524,7 +534,7 @@ def moe_block_norm_bwd(dims, cfg, dn, dres_out, y, u, w_post, gate, w_pre, dy, d
                                   _need("dw_post", dw_post, f32, d, dev),
                                   _need("dgate", dgate, f32, g, dev),
                                   _need("dw_pre", dw_pre, f32, d, dev), int(accumulate),
-                                  *_bytes("ws", ws, dev), _s(stream)), "moe_block_norm_bwd")
+                                  *_bytes("ws", ws, dev), _here(stream, dev)), "moe_block_norm_bwd")
 
 
 # ---------------------------------------------------------- gradient clipping --
@@ -560,7 +570,7 @@ def moe_grad_norm(grads, accumulate, sumsq, norm, ws, stream=None):
     _ck(load().moe_grad_norm(ctypes.addressof(grads.array), len(grads), int(accumulate),
                              _need("sumsq", sumsq, y["f64"], 1, dev),
                              _need("norm", norm, y["f32"], 1, dev), *_bytes("ws", ws, dev),
-                             _s(stream)), "moe_grad_norm")
+                             _here(stream, dev)), "moe_grad_norm")
 
 
 def moe_grad_clip(grads, sumsq, max_norm, norm, coef, stream=None):
@@ -569,7 +579,8 @@ def moe_grad_clip(grads, sumsq, max_norm, norm, coef, stream=None):
     _ck(load().moe_grad_clip(ctypes.addressof(grads.array), len(grads),
                              _need("sumsq", sumsq, y["f64"], 1, dev), float(max_norm),
                              _need("norm", norm, y["f32"], 1, dev),
-                             _need("coef", coef, y["f32"], 1, dev), _s(stream)), "moe_grad_clip")
+                             _need("coef", coef, y["f32"], 1, dev), _here(stream, dev)),
+        "moe_grad_clip")
 
 
 def moe_grad_clip_norm(grads, max_norm, sumsq, norm, coef, ws, stream=None):
@@ -579,4 +590,4 @@ def moe_grad_clip_norm(grads, max_norm, sumsq, norm, coef, ws, stream=None):
                                   _need("sumsq", sumsq, y["f64"], 1, dev),
                                   _need("norm", norm, y["f32"], 1, dev),
                                   _need("coef", coef, y["f32"], 1, dev), *_bytes("ws", ws, dev),
-                                  _s(stream)), "moe_grad_clip_norm")
+                                  _here(stream, dev)), "moe_grad_clip_norm")

@@ -11,11 +11,13 @@
 // computed in FP32 with a bound on their error (margins below), and the order found stands
 // where neighbouring scores differ by more than the bound, or by nothing in 64 bits
 // either (equal logits and biases).  Where the check fails, about one token in a thousand,
-// the few experts in question are ordered by their scores in 64 bits (refine); only tokens
-// beyond FP32's range, or without a clear choice of groups, are done in 64 bits whole.  What bounds the calls is instruction issue (about
+// the few experts in question are ordered by their scores in 64 bits (refine), and so are
+// groups (refine_groups); only tokens beyond FP32's range are done in 64 bits whole.  What bounds the calls is instruction issue (about
 // 250 a token for 128 experts), so a pick costs one reduction, a ballot and a few selects:
 // each lane keeps its two best scores, and which expert a pick was is looked up once, by
 // lane j for pick j.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -169,11 +171,19 @@ __device__ __forceinline__ void get(const V* sh, int lane, V (&v)[EPL]) {
 union RouteShared {
   double f64[2 * RT_EMAX];  // scores and group scores
   struct {
-    // by slot (keep_groups before: scores and group scores; refine after: candidates)
-    uint32_t key[RT_EMAX];  // ordered scores
-    float p[RT_EMAX];       // affinities
+    uint32_t key[RT_EMAX];  // ordered scores, by slot (refine: the experts in question)
+    float p[RT_EMAX];       // affinities, by slot
     uint2 pick[32];         // key and lane of a pick
   } f32;
+  struct {
+    union {
+      double s64[RT_EMAX];  // scores by expert, then group scores
+      struct {
+        float s[RT_EMAX], score[RT_EMAX];
+      };
+    };
+    int keep[RT_EMAX];
+  } group;
 };
 
 // A token in 64 bits: the definition itself, in little code rather than little time.
@@ -343,11 +353,77 @@ struct Best {
   }
 };
 
-// Gives the experts of groups that are not kept the score -inf; false where FP32 cannot
-// tell which groups stay.  two_dp: twice an affinity's error.
-template <int EPL>
-__device__ __forceinline__ bool keep_groups(const RouteArgs& a, RouteShared& sh, float (&s)[EPL],
-                                            float two_dp) {
+// Which groups stay, in 64 bits where FP32 does not settle it: a group's lanes share its
+// experts (one lane a group where there are more than 16).
+template <typename LT>
+__device__ __noinline__ void refine_groups(const RouteArgs& a, const LT* row, float m,
+                                           RouteShared& sh) {
+  const int lane = threadIdx.x & 31, size = a.E / a.n_group;
+  double z = 0.0, rz = 1.0;
+  __syncwarp();
+#pragma unroll 2
+  for (int e = lane; e < a.E; e += 32) {
+    const double x = load1(row + e), v = exp(a.softmax ? x - (double)m : -x);
+    const double p = a.softmax ? v : 1.0 / (1.0 + v);
+    sh.group.s64[e] = p;
+    z += p;
+  }
+  if (a.softmax) rz = 1.0 / warp_sum(z);
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 32) {
+    const double s = sh.group.s64[e] * rz + (a.bias ? (double)a.bias[e] : 0.0);
+    sh.group.s64[e] = load1(row + e) == -INFINITY || s != s ? -INFINITY : s;
+  }
+  __syncwarp();
+  int share = 1;  // lanes of a group
+  while (share * 2 * a.n_group <= 32) share *= 2;
+  const int at = lane & (share - 1);
+  double score[RT_EMAX / 32];  // of this lane's groups
+#pragma unroll
+  for (int i = 0; i < RT_EMAX / 32; ++i) {
+    const int g = lane / share + i * (32 / share);
+    if (i * 32 >= a.n_group * share) break;
+    double b1 = -INFINITY, b2 = -INFINITY;
+    if (g < a.n_group)
+#pragma unroll 4
+      for (int n = at; n < size; n += share) {
+        const double v = sh.group.s64[g * size + n];
+        b2 = fmax(b2, fmin(b1, v));
+        b1 = fmax(b1, v);
+      }
+    for (int o = 1; o < share; o <<= 1) {
+      const double o1 = __shfl_xor_sync(FULL, b1, o), o2 = __shfl_xor_sync(FULL, b2, o);
+      b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+      b1 = fmax(b1, o1);
+    }
+    score[i] = a.group_top == 2 ? b1 + b2 : b1;
+  }
+  __syncwarp();
+  double* of_group = sh.group.s64;
+#pragma unroll
+  for (int i = 0; i < RT_EMAX / 32; ++i) {
+    const int g = lane / share + i * (32 / share);
+    if (at == 0 && g < a.n_group && i * 32 < a.n_group * share) of_group[g] = score[i];
+  }
+  __syncwarp();
+#pragma unroll 1
+  for (int g = lane; g < a.n_group; g += 32) {
+    const double mine = of_group[g];
+    int before = 0;
+#pragma unroll 4
+    for (int h = 0; h < a.n_group; ++h) {
+      const double v = of_group[h];
+      before += v > mine || (v == mine && h < g);
+    }
+    sh.group.keep[g] = before < a.topk_group;
+  }
+}
+
+// Gives the experts of groups that are not kept the score -inf.  two_dp: twice an
+// affinity's error; m: the largest logit, for refine_groups.
+template <typename LT, int EPL>
+__device__ __forceinline__ void keep_groups(const RouteArgs& a, const LT* row, float m,
+                                            RouteShared& sh, float (&s)[EPL], float two_dp) {
   const int lane = threadIdx.x & 31, e0 = lane * EPL;
   const int size = a.E / a.n_group, lanes = size / EPL;
   // of the groups that this lane compares, ordered: the lowest score kept, less its error,
@@ -359,6 +435,11 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, RouteShared& sh,
     const float t = a.group_top == 2 ? fabsf(b1) + fabsf(b2) : fabsf(b1);
     err = two_dp + (t < INFINITY ? 0x1p-22f * t : 0.0f);
     return a.group_top == 2 ? b1 + b2 : b1;
+  };
+  auto clear = [&]() {
+    const float lo = unordered(__reduce_min_sync(FULL, low));
+    const uint32_t most = __reduce_max_sync(FULL, high);
+    return lo > unordered(most) || most <= ORD_NEG_INF;
   };
   auto sort_out = [&](float mine, bool keep) {
     if (keep) low = min(low, ordered(mine - err));
@@ -387,18 +468,20 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, RouteShared& sh,
       before += (v > mine || (v == mine && o < at)) && h + lane - at < a.n_group;
     }
     for (int o = 1; o < lanes; o <<= 1) before += __shfl_xor_sync(FULL, before, o);
-    if (e0 < a.E) {
-      const bool keep = before < a.topk_group;
-      sort_out(mine, keep);
+    const bool keep = before < a.topk_group;
+    if (e0 < a.E) sort_out(mine, keep);
+    if (clear()) {
       if (!keep) {
 #pragma unroll
         for (int q = 0; q < EPL; ++q) s[q] = -INFINITY;
       }
+      return;
     }
+    refine_groups(a, row, m, sh);
   } else {
     // lane g % 32 looks after group g
-    float* all = reinterpret_cast<float*>(sh.f32.key);
-    float* of_group = sh.f32.p;
+    float* all = sh.group.s;
+    float* of_group = sh.group.score;
     constexpr int MOST = RT_EMAX / 32;
     float mine[MOST], off[MOST];
 #pragma unroll
@@ -434,24 +517,25 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, RouteShared& sh,
       kept |= (before < a.topk_group ? 1u : 0u) << i;
     }
     __syncwarp();
+    if (clear()) {
 #pragma unroll
-    for (int i = 0; i < MOST; ++i)
-      if (lane + 32 * i < a.n_group) of_group[lane + 32 * i] = kept >> i & 1 ? INFINITY : -INFINITY;
-    __syncwarp();
-    int g = e0 / size, left = size - (e0 - g * size);  // the next expert's group
-#pragma unroll
-    for (int q = 0; q < EPL; ++q) {
-      if (e0 + q < a.E) s[q] = fminf(s[q], of_group[g]);
-      if (--left == 0) {
-        left = size;
-        ++g;
-      }
+      for (int i = 0; i < MOST; ++i)
+        if (lane + 32 * i < a.n_group) sh.group.keep[lane + 32 * i] = kept >> i & 1;
+    } else {
+      refine_groups(a, row, m, sh);
     }
-    __syncwarp();
   }
-  const float lo = unordered(__reduce_min_sync(FULL, low));
-  const uint32_t most = __reduce_max_sync(FULL, high);
-  return lo > unordered(most) || most <= ORD_NEG_INF;
+  __syncwarp();
+  int g = e0 / size, left = size - (e0 - g * size);  // the next expert's group
+#pragma unroll
+  for (int q = 0; q < EPL; ++q) {
+    if (e0 + q < a.E && !sh.group.keep[g]) s[q] = -INFINITY;
+    if (--left == 0) {
+      left = size;
+      ++g;
+    }
+  }
+  __syncwarp();
 }
 
 // The picks' order in 64 bits where FP32 does not settle it: of the experts whose keys are
@@ -514,11 +598,11 @@ __device__ __noinline__ bool refine(const RouteArgs& a, const LT* row, float m, 
 //            p (|x - m| + 25) u <= 25 u max p, the largest where x = m.
 // Twice that is 6 u and 50 u / z; the margins take 8 u and 64 u / z.  Adding the bias rounds
 // by u |score|; 2 u a score stand in the margin.
-template <typename LT, int EPL, bool SOFT, bool VEC>
+template <typename LT, int EPL, bool SOFT, bool VEC, bool GROUPS>
 __device__ __forceinline__ bool route_token(const RouteArgs& a, int64_t t, RouteShared& sh) {
   const int lane = threadIdx.x & 31, e0 = lane * EPL;
   const LT* row = reinterpret_cast<const LT*>(a.logits) + t * a.E;
-  const bool bias = a.bias != nullptr, groups = a.n_group > 1;
+  const bool bias = a.bias != nullptr;
   auto here = [&](int q) { return VEC ? e0 < a.E : e0 + q < a.E; };
   float x[EPL], b[EPL];
   load_row(x, row, e0, a.E, VEC, -INFINITY);
@@ -546,19 +630,19 @@ __device__ __forceinline__ bool route_token(const RouteArgs& a, int64_t t, Route
   if (a.probs) store_row(a.probs + t * a.E, s, e0, a.E, VEC);
   const float two_dp = SOFT ? 0x1p-18f * rz : 0x1p-21f;
   // scores; without a bias the logits rank the experts, exactly
-  if (bias || groups) {
+  if (bias || GROUPS) {
 #pragma unroll
     for (int q = 0; q < EPL; ++q) {
       if (!SOFT) s[q] = p[q];
       if (bias) s[q] = fmaxf(s[q] + b[q], -INFINITY);  // a NaN ranks as -inf
       if (x[q] == -INFINITY) s[q] = -INFINITY;
     }
-    if (groups && !keep_groups(a, sh, s, two_dp)) return false;
+    if constexpr (GROUPS) keep_groups(a, row, m, sh, s, two_dp);
   }
   if (!bias) {
 #pragma unroll
     for (int q = 0; q < EPL; ++q)
-      if (!groups || s[q] != -INFINITY) s[q] = x[q];
+      if (!GROUPS || s[q] != -INFINITY) s[q] = x[q];
   }
   uint32_t u[EPL];
 #pragma unroll
@@ -654,7 +738,9 @@ __device__ __forceinline__ bool route_token(const RouteArgs& a, int64_t t, Route
   return true;
 }
 
-template <typename LT, int EPL, bool SOFT, bool VEC>
+// A warp a token: a loop over tokens with the next one's logits on their way took 1.5 times
+// as long, since its state does not fit the registers beside the calls.
+template <typename LT, int EPL, bool SOFT, bool VEC, bool GROUPS>
 __global__ void __launch_bounds__(RT_WARPS * 32, EPL == 8 ? 8 : 10)
     route_topk_kernel(const RouteArgs a) {
   __shared__ __align__(16) RouteShared sh[RT_WARPS];
@@ -662,7 +748,7 @@ __global__ void __launch_bounds__(RT_WARPS * 32, EPL == 8 ? 8 : 10)
   const int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp;
   if (t >= a.T) return;
   // lane j looks after pick j: more than 32 picks take the 64-bit way
-  if (a.k > 32 || !route_token<LT, EPL, SOFT, VEC>(a, t, sh[warp]))
+  if (a.k > 32 || !route_token<LT, EPL, SOFT, VEC, GROUPS>(a, t, sh[warp]))
     route_token_f64<LT>(a, t, sh[warp]);
 }
 
@@ -754,72 +840,80 @@ __device__ __noinline__ void route_bwd_f64(const RouteBwdArgs& a, int64_t t, dou
 }
 
 // A token with at most 32 picks, lane j looking after pick j; false where its affinities
-// leave FP32's range.  dp: the affinities, then the picks' dp by slot,
-// in shared memory.
-template <typename LT, int EPL, bool SOFT, bool VEC>
-__device__ __forceinline__ bool route_bwd_token(const RouteBwdArgs& a, int64_t t, float* dp) {
+// leave FP32's range.  sh: [2][RT_EMAX], by slot.  What bounds it is latency, so the sums
+// run side by side: a softmax's sum of p dp over the picks comes from that of p dw.
+template <typename LT, int EPL, bool SOFT, bool VEC, bool SEQ>
+__device__ __forceinline__ bool route_bwd_token(const RouteBwdArgs& a, int64_t t, float* sh) {
   const int lane = threadIdx.x & 31, e0 = lane * EPL;
   const LT* row = reinterpret_cast<const LT*>(a.logits) + t * a.E;
-  // pick j
   const bool mine = lane < a.k;
   const int e = mine ? a.idx[t * a.k + lane] : -1;
   const float wj = mine ? a.w[t * a.k + lane] : 0.0f, dwj = mine ? a.dw[t * a.k + lane] : 0.0f;
   const bool ok = wj != 0.0f && e >= 0 && e < a.E;
-  const bool seq = a.seq_grad != nullptr;
+  const int se = ok ? slot<EPL>(e / EPL, e % EPL) : 0;
+  float* ps = sh;            // affinities
+  float* dp = sh + RT_EMAX;  // the picks' dp
   float x[EPL], sg[EPL];
   load_row(x, row, e0, a.E, VEC, -INFINITY);
-  if (seq) load_row(sg, a.seq_grad + (t / a.seq_len) * a.E, e0, a.E, VEC, 0.0f);
+  if (SEQ) {
+    const uint32_t len = (uint32_t)min(a.seq_len, (int64_t)0x7fffffff);  // T is below 2^31
+    load_row(sg, a.seq_grad + (int64_t)((uint32_t)t / len) * a.E, e0, a.E, VEC, 0.0f);
+  }
+  // does an expert stand twice among the picks?
+  if (ok) dp[se] = __int_as_float(lane);
+  __syncwarp();
+  const bool twice = __any_sync(FULL, ok && __float_as_int(dp[se]) != lane);
+  float g[EPL];
+#pragma unroll
+  for (int q = 0; q < EPL; ++q) g[q] = 0.0f;
+  put(dp, lane, g);
+  // affinities, of a softmax times their sum z
   float p[EPL], s1[EPL];  // s1: p (1 - p) of a sigmoid, without the cancellation of 1 - p
-  float z = 0.0f, rz = 0.0f;
+  float m = 0.0f;
   if (SOFT) {
-    float m = x[0];
+    m = x[0];
 #pragma unroll
     for (int q = 1; q < EPL; ++q) m = fmaxf(m, x[q]);
     m = warp_max(m);
     if (m == -INFINITY) m = 0.0f;
+  }
 #pragma unroll
-    for (int q = 0; q < EPL; ++q) {
+  for (int q = 0; q < EPL; ++q) {
+    if (SOFT) {
       p[q] = expf(x[q] - m);
-      z += p[q];
-    }
-    z = warp_sum(z);
-    rz = z == 0.0f ? 0.0f : quick_rcp(z);
-#pragma unroll
-    for (int q = 0; q < EPL; ++q) p[q] *= rz;
-  } else {
-#pragma unroll
-    for (int q = 0; q < EPL; ++q) {
+    } else {
       const float h = expf(-fabsf(x[q])), r = quick_rcp(1.0f + h);
       p[q] = x[q] >= 0.0f ? r : x[q] < 0.0f ? h * r : x[q];
       s1[q] = h * r * r;
-      z += p[q];
-    }
-    if (seq) {
-      z = warp_sum(z);
-      if (z < RT_SMALL_ALL) return false;
-      rz = quick_rcp(z);
     }
   }
-  put(dp, lane, p);
+  put(ps, lane, p);
   __syncwarp();
-  const int se = ok ? slot<EPL>(e / EPL, e % EPL) : 0;
-  const float pe = ok ? dp[se] : 0.0f;
-  __syncwarp();
-  float g[EPL], c = 0.0f;
+  const float pe = ok ? ps[se] : 0.0f;
+  // all sums in one round: over the picks p, dw w and p dw, over the experts p and p g
+  float sum[5] = {pe, ok ? dwj * wj : 0.0f, ok ? pe * dwj : 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int q = 0; q < EPL; ++q) g[q] = 0.0f;
-  put(dp, lane, g);
-  float d = a.scale * dwj;
-  if (a.renorm) {
-    const float zc = warp_sum(pe), dot = warp_sum(ok ? dwj * wj : 0.0f);
-    if (__any_sync(FULL, ok) && zc < RT_SMALL_SUM) return false;
-    d = (d - dot) / zc;
+  for (int q = 0; q < EPL; ++q) {
+    sum[3] += p[q];
+    if (SEQ) sum[4] = fmaf(p[q], sg[q], sum[4]);
   }
-  __syncwarp();
-  // an expert that stands twice among the picks gets both terms, in the picks' order
-  const unsigned same = __match_any_sync(FULL, ok ? e : -1 - lane);
-  const bool first = ok && (same & ((1u << lane) - 1)) == 0;
-  if (__any_sync(FULL, ok && same != (1u << lane))) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) sum[i] += __shfl_xor_sync(FULL, sum[i], o);
+  const float z = sum[3], rz = z == 0.0f ? 0.0f : quick_rcp(z);
+  if (!SOFT && SEQ && z < RT_SMALL_ALL) return false;
+  const bool any = __any_sync(FULL, ok);
+  const float unit = SOFT ? rz : 1.0f;  // of p
+  float d = a.scale * dwj, cp = a.scale * sum[2] * unit;  // cp: sum of p dp over the picks
+  if (a.renorm) {
+    if (any && sum[0] < RT_SMALL_SUM) return false;
+    const float r = any ? 1.0f / sum[0] : 0.0f;  // 1 / sum of the picks' p z
+    d = (d - sum[1]) * r * (SOFT ? z : 1.0f);
+    cp = a.scale * sum[2] * r - (any ? sum[1] : 0.0f);
+  }
+  if (twice) {  // both terms, in the picks' order
+    const unsigned same = __match_any_sync(FULL, ok ? e : -1 - lane);
     float v = 0.0f;
     for (int j = 0; j < a.k; ++j) {
       const float o = __shfl_sync(FULL, d, j);
@@ -827,39 +921,29 @@ __device__ __forceinline__ bool route_bwd_token(const RouteBwdArgs& a, int64_t t
     }
     d = v;
   }
-  if (first) dp[se] = d;
+  if (ok) dp[se] = d;
   __syncwarp();
   get(dp, lane, g);
-  if (seq) {
-    float cg = 0.0f;
-    if (!SOFT) {
+  const float cg = SEQ ? sum[4] * rz : 0.0f;  // of the affinities that sum to 1
 #pragma unroll
-      for (int q = 0; q < EPL; ++q) cg += p[q] * rz * sg[q];
-      cg = warp_sum(cg);
-    }
-#pragma unroll
-    for (int q = 0; q < EPL; ++q) g[q] += SOFT ? sg[q] : (sg[q] - cg) * rz;
+  for (int q = 0; q < EPL; ++q) {
+    if (SOFT) g[q] = p[q] * rz * (SEQ ? g[q] + sg[q] - (cp + cg) : g[q] - cp);
+    else g[q] = s1[q] * (SEQ ? g[q] + (sg[q] - cg) * rz : g[q]);
   }
-  if (SOFT) {
-#pragma unroll
-    for (int q = 0; q < EPL; ++q) c += p[q] * g[q];
-    c = warp_sum(c);
-  }
-#pragma unroll
-  for (int q = 0; q < EPL; ++q) g[q] = SOFT ? p[q] * (g[q] - c) : g[q] * s1[q];
   store_row(reinterpret_cast<LT*>(a.dlogits) + t * a.E, g, e0, a.E, VEC);
   return true;
 }
 
-template <typename LT, int EPL, bool SOFT, bool VEC>
+template <typename LT, int EPL, bool SOFT, bool VEC, bool SEQ>
 __global__ void __launch_bounds__(RT_WARPS * 32, EPL == 8 ? 8 : 10)
     route_bwd_kernel(const RouteBwdArgs a) {
-  __shared__ __align__(16) double dp[RT_WARPS][RT_EMAX];
+  __shared__ __align__(16) double sh[RT_WARPS][RT_EMAX];
   const int warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp;
   if (t >= a.T) return;
-  if (a.k > 32 || !route_bwd_token<LT, EPL, SOFT, VEC>(a, t, reinterpret_cast<float*>(dp[warp])))
-    route_bwd_f64<LT>(a, t, dp[warp]);
+  float* f32 = reinterpret_cast<float*>(sh[warp]);
+  if (a.k > 32 || !route_bwd_token<LT, EPL, SOFT, VEC, SEQ>(a, t, f32))
+    route_bwd_f64<LT>(a, t, sh[warp]);
 }
 
 // Whether rows of E experts from p on can be taken EPL at a time: whole pieces that start
@@ -870,21 +954,35 @@ bool in_pieces(const void* p, int E, int size) {
   return E % epl == 0 && reinterpret_cast<uintptr_t>(p) % piece == 0;
 }
 
+// Launches the kernel for a call's settings, as compile-time values.
+template <typename F>
+void settle(bool v, F f) {
+  if (v) f(std::true_type{});
+  else f(std::false_type{});
+}
 template <typename LT, int EPL>
 void start(const RouteArgs& a, cudaStream_t st) {
-  const unsigned blocks = (unsigned)((a.T + RT_WARPS - 1) / RT_WARPS), threads = RT_WARPS * 32;
-  if (a.softmax && a.vec) route_topk_kernel<LT, EPL, true, true><<<blocks, threads, 0, st>>>(a);
-  else if (a.softmax) route_topk_kernel<LT, EPL, true, false><<<blocks, threads, 0, st>>>(a);
-  else if (a.vec) route_topk_kernel<LT, EPL, false, true><<<blocks, threads, 0, st>>>(a);
-  else route_topk_kernel<LT, EPL, false, false><<<blocks, threads, 0, st>>>(a);
+  const unsigned blocks = (unsigned)((a.T + RT_WARPS - 1) / RT_WARPS);
+  settle(a.softmax, [&](auto soft) {
+    settle(a.vec, [&](auto vec) {
+      settle(a.n_group > 1, [&](auto groups) {
+        route_topk_kernel<LT, EPL, soft.value, vec.value, groups.value>
+            <<<blocks, RT_WARPS * 32, 0, st>>>(a);
+      });
+    });
+  });
 }
 template <typename LT, int EPL>
 void start(const RouteBwdArgs& a, cudaStream_t st) {
-  const unsigned blocks = (unsigned)((a.T + RT_WARPS - 1) / RT_WARPS), threads = RT_WARPS * 32;
-  if (a.softmax && a.vec) route_bwd_kernel<LT, EPL, true, true><<<blocks, threads, 0, st>>>(a);
-  else if (a.softmax) route_bwd_kernel<LT, EPL, true, false><<<blocks, threads, 0, st>>>(a);
-  else if (a.vec) route_bwd_kernel<LT, EPL, false, true><<<blocks, threads, 0, st>>>(a);
-  else route_bwd_kernel<LT, EPL, false, false><<<blocks, threads, 0, st>>>(a);
+  const unsigned blocks = (unsigned)((a.T + RT_WARPS - 1) / RT_WARPS);
+  settle(a.softmax, [&](auto soft) {
+    settle(a.vec, [&](auto vec) {
+      settle(a.seq_grad != nullptr, [&](auto seq) {
+        route_bwd_kernel<LT, EPL, soft.value, vec.value, seq.value>
+            <<<blocks, RT_WARPS * 32, 0, st>>>(a);
+      });
+    });
+  });
 }
 
 template <typename LT, typename Args>
