@@ -56,7 +56,7 @@ class EPBuffers:
     ``recv_rows_cap``), its y / dxp rows beyond ``loc.Rr`` the shared experts' own.
 
     recv_rows_cap defaults to the most a rank can receive:
-    W · (T · min(k, E_l) + E_l · (P - 1)).
+    W · (T · min(k, E_l) + E_l · (P - 1)).  ``route``: as in MoEBuffers.
 
     ``alloc(shape, dtype)`` allocates the buffers other ranks write into (default: plain
     device memory); they are ``ep_ws``, ``loc.x_perm``, ``full.y`` and, for training,
@@ -64,7 +64,7 @@ class EPBuffers:
     rank every rank's addresses of them."""
 
     def __init__(self, dims: L.MoeDims, rank: int, world: int, train: bool = False,
-                 device="cuda", recv_rows_cap: int | None = None, alloc=None):
+                 device="cuda", recv_rows_cap: int | None = None, alloc=None, route=None):
         if dims.E % world:
             raise ValueError(f"E = {dims.E} experts do not split over {world} ranks")
         if not 1 <= world <= L.MOE_EP_MAX_WORLD:
@@ -77,7 +77,8 @@ class EPBuffers:
                                      dims.P, cap)
         dev = torch.device(device)
         alloc = alloc or (lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev))
-        self.full = MoEBuffers(dims, device=dev, train=train, experts=False, gather=True)
+        self.full = MoEBuffers(dims, device=dev, train=train, experts=False, gather=True,
+                               route=route)
         self.loc = MoEBuffers(self.dims_loc, device=dev, train=train)
         bf = torch.bfloat16
         d = dims.d
@@ -163,8 +164,7 @@ def route(eb: EPBuffers, x, wg, bias, stream=None, seq_balance=None):
     (and the sequence-wise balance loss with ``seq_balance``)."""
     F = eb.full
     dm = F.dims
-    L.moe_gate_topk(dm, x, wg, bias, F.topk_idx, F.topk_w, F.probs if eb.train else None, F.ws,
-                    stream)
+    layer.gate(F, x, wg, bias, stream)
     L.moe_permute_align(dm, F.topk_idx, None, F.counts, F.offsets, F.sorted_ids, F.row_of,
                         None, F.ws, stream)
     if eb.train:
@@ -239,12 +239,7 @@ def unpermute_and_router(eb: EPBuffers, x, wg=None, stream=None):
     L.moe_ep_wait(eb.peers["ws"], L.MOE_EP_WAIT_DX, stream)
     L.moe_combine_split(F.dims, F.dxp, Lc.dxp[Lc.Rr:], F.row_of, None, F.dx, stream)
     if wg is not None:
-        if F.bal_seq_len is not None:
-            L.moe_router_bwd_seqbal(F.dims, x, wg, F.probs, F.topk_idx, F.topk_w, F.dw_comb,
-                                    F.bal_grad, F.bal_seq_len, None, F.dx, F.dwg, 0, F.ws, stream)
-        else:
-            L.moe_router_bwd(F.dims, x, wg, F.probs, F.topk_idx, F.topk_w, F.dw_comb, None, F.dx,
-                             F.dwg, 0, F.ws, stream)
+        layer.gate_backward(F, x, wg, stream)
     return F.dx
 
 

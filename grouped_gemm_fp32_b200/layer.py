@@ -16,6 +16,11 @@ and "Load balancing"; §3.2 "Efficient implementation of Grouped GEMM"):
               [-> moe_bias_update (next step's selection bias)]
 The router backward runs when the gate weights are passed to ``backward``; the
 bias step when an update speed ``gamma`` is.
+With ``MoEBuffers(route=MoeRouteCfg...)`` the router is one of other kinds (sigmoid
+scores, expert groups, a factor on the weights): moe_gate_logits -> moe_route_topk takes
+the place of moe_gate_topk, and moe_route_bwd -> moe_gate_bwd that of moe_router_bwd.
+``block_forward`` and ``block_backward`` run the layer between the norms of a
+transformer block (moe_block_norm); ``GradClip`` clips the gradients by their global norm.
 Under token data parallelism, ``dp_bias_step`` (the bias step on the whole batch's
 loads) and ``dp_allreduce_grads`` (the weight gradients' sum) exchange what the
 ranks share, over torch.distributed.
@@ -31,7 +36,7 @@ from . import _lib as L
 
 class MoEBuffers:
     def __init__(self, dims: L.MoeDims, device="cuda", train: bool = False,
-                 gather: bool = False, experts: bool = True):
+                 gather: bool = False, experts: bool = True, route: L.MoeRouteCfg | None = None):
         """``gather``: the first GEMM (and dW1) read the routed x rows straight from x
         through ``sorted_ids`` (grouped_gemm_fwd_gather / grouped_gemm_bwd_dw1_gather)
         and no x_perm [Rr, d] is allocated; otherwise (the default, faster on B200:
@@ -40,10 +45,13 @@ class MoEBuffers:
         ``experts=False``: the buffers of a rank whose routed rows are computed
         elsewhere (expert parallelism): routing, permutation, combine and router
         buffers, with y, dy and dxp holding the routed rows only [Rr, d]; no
-        expert activations (h, a1, da) and no expert weight gradients."""
+        expert activations (h, a1, da) and no expert weight gradients.
+        ``route``: how the router scores and chooses (None: the layer's own, softmax over
+        all experts); adds the logits [T, E] and, for training, their gradient."""
         self.dims = dims
         self.train = train
         self.gather = gather
+        self.route = route
         T, d, E, k, S, I = dims.T, dims.d, dims.E, dims.k, dims.S, dims.I
         G = E + S
         self.Rr = L.moe_rows_routed(dims)
@@ -54,6 +62,8 @@ class MoEBuffers:
         i32, f32, bf = torch.int32, torch.float32, torch.bfloat16
         e = lambda *s, dt=bf: torch.empty(*s, dtype=dt, device=dev)
         self.ws = torch.zeros(L.moe_workspace_size(dims), dtype=torch.uint8, device=dev)
+        self.logits = e(T, E, dt=f32) if route is not None else None
+        self.logits_valid = False      # the last forward's router wrote them
         self.topk_idx = e(T, k, dt=i32)
         self.topk_w = e(T, k, dt=f32)
         self.counts = e(E, dt=i32)
@@ -75,6 +85,7 @@ class MoEBuffers:
             self.dw1 = e(G, 2 * I, d, dt=f32) if experts else None
             self.dw2 = e(G, d, I, dt=f32) if experts else None
             self.probs = e(T, E, dt=f32)
+            self.dlogits = e(T, E, dt=f32) if route is not None else None
             self.dwg = e(E, d, dt=f32)
             self.bias_next = e(E, dt=f32)
             # sequence-wise balance loss: its value and dL/dp per sequence (sequences
@@ -86,6 +97,37 @@ class MoEBuffers:
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in vars(self).values()
                    if isinstance(t, torch.Tensor))
+
+
+def gate(b: MoEBuffers, x, wg, bias, stream=None):
+    """The router's choice for x: b.topk_idx, b.topk_w and, for training, b.probs."""
+    dm = b.dims
+    probs = b.probs if b.train else None
+    if b.route is None:
+        L.moe_gate_topk(dm, x, wg, bias, b.topk_idx, b.topk_w, probs, b.ws, stream)
+    else:
+        L.moe_gate_logits(dm, x, wg, b.logits, b.ws, stream)
+        L.moe_route_topk(dm, b.route, b.logits, bias, b.topk_idx, b.topk_w, probs, stream)
+        b.logits_valid = True
+
+
+def gate_backward(b: MoEBuffers, x, wg, stream=None):
+    """The router's backward after the combine's: its term is added to b.dx, and b.dwg
+    receives dL/dWg."""
+    dm = b.dims
+    seq_grad, seq_len = (b.bal_grad, b.bal_seq_len) if b.bal_seq_len is not None else (None, 0)
+    if b.route is not None:
+        if not b.logits_valid:
+            raise ValueError("the router's backward needs a forward that ran the router")
+        L.moe_route_bwd(dm, b.route, b.logits, b.topk_idx, b.topk_w, b.dw_comb, seq_grad, seq_len,
+                        b.dlogits, stream)
+        L.moe_gate_bwd(dm, x, wg, b.dlogits, b.dx, b.dwg, 0, b.ws, stream)
+    elif seq_grad is not None:
+        L.moe_router_bwd_seqbal(dm, x, wg, b.probs, b.topk_idx, b.topk_w, b.dw_comb, seq_grad,
+                                seq_len, None, b.dx, b.dwg, 0, b.ws, stream)
+    else:
+        L.moe_router_bwd(dm, x, wg, b.probs, b.topk_idx, b.topk_w, b.dw_comb, None, b.dx, b.dwg,
+                         0, b.ws, stream)
 
 
 def forward(b: MoEBuffers, x, wg, bias, w1, w2, stream=None, routing=None, seq_balance=None):
@@ -100,8 +142,9 @@ def forward(b: MoEBuffers, x, wg, bias, w1, w2, stream=None, routing=None, seq_b
     dm = b.dims
     probs = b.probs if b.train else None
     if routing is None:
-        L.moe_gate_topk(dm, x, wg, bias, b.topk_idx, b.topk_w, probs, b.ws, stream)
+        gate(b, x, wg, bias, stream)
     else:
+        b.logits_valid = False
         b.topk_idx.copy_(routing[0])
         b.topk_w.copy_(routing[1])
         if probs is not None and len(routing) > 2:
@@ -142,12 +185,7 @@ def backward(b: MoEBuffers, x, dout, w1, w2, stream=None, wg=None, gamma=None, b
         L.grouped_gemm_bwd_dw(dm, b.ws, L.MOE_GEMM1, b.da, None, b.x_perm, x, b.dw1, 0, stream)
     L.moe_combine(dm, b.dxp, b.row_of, None, b.dx, stream)
     if wg is not None:
-        if b.bal_seq_len is not None:
-            L.moe_router_bwd_seqbal(dm, x, wg, b.probs, b.topk_idx, b.topk_w, b.dw_comb,
-                                    b.bal_grad, b.bal_seq_len, None, b.dx, b.dwg, 0, b.ws, stream)
-        else:
-            L.moe_router_bwd(dm, x, wg, b.probs, b.topk_idx, b.topk_w, b.dw_comb, None, b.dx,
-                             b.dwg, 0, b.ws, stream)
+        gate_backward(b, x, wg, stream)
     if gamma is not None:
         L.moe_bias_update(dm, b.counts, gamma, bias, b.bias_next, stream)
     return b.dx, b.dw1, b.dw2, b.dw_comb
@@ -208,6 +246,124 @@ def dp_allreduce_grads(grads, group=None, stream=None):
     return grads
 
 
+# -------------------------------------------------------------- global clipping --
+class GradClip:
+    """Clipping of gradients that stay where they are by their global norm, on the
+    device: ``GradClip(grads)``, then ``clip(max_norm)`` every step.
+
+    ``sharded``: tensors that this rank alone holds of the model's (under expert
+    parallelism the routed experts' dW); their squares are added over ``group``.
+    ``grads`` are whole on every rank (after ``dp_allreduce_grads``) and count once.
+    ``outs`` / ``sharded_outs``: where the clipped gradients go (None: in place)."""
+
+    def __init__(self, grads, outs=None, sharded=(), sharded_outs=None, group=None):
+        self.whole = L.GradList(grads, outs)
+        self.shards = L.GradList(sharded, sharded_outs) if len(sharded) else None
+        self.group = group
+        every = self.whole.grads + (self.shards.grads if self.shards else [])
+        if not every:
+            raise ValueError("no gradients to clip")
+        dev = every[0].device
+        self.sumsq = torch.zeros(1, dtype=torch.float64, device=dev)
+        self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
+        self.coef = torch.zeros(1, dtype=torch.float32, device=dev)
+        n = max(len(self.whole), len(self.shards) if self.shards else 0)
+        self.ws = torch.empty(L.moe_grad_workspace_size(n), dtype=torch.uint8, device=dev)
+
+    def clip(self, max_norm, stream=None):
+        """Scales every gradient by min(1, max_norm / (norm + 1e-6)).  Returns ``norm`` [1]
+        f32, the norm before; ``coef`` [1] holds the factor.  Nothing comes to the host."""
+        if self.shards is None:
+            L.moe_grad_clip_norm(self.whole, max_norm, self.sumsq, self.norm, self.coef, self.ws,
+                                 stream)
+            return self.norm
+        import torch.distributed as dist
+        L.moe_grad_norm(self.shards, 0, self.sumsq, None, self.ws, stream)
+        with on_stream(stream):
+            dist.all_reduce(self.sumsq, op=dist.ReduceOp.SUM, group=self.group)
+        L.moe_grad_norm(self.whole, 1, self.sumsq, None, self.ws, stream)
+        L.moe_grad_clip(self.shards, self.sumsq, max_norm, self.norm, self.coef, stream)
+        L.moe_grad_clip(self.whole, self.sumsq, max_norm, None, None, stream)
+        return self.norm
+
+
+# ---------------------------------------------------------------- a block --
+# The layer as a transformer block's second half:
+#   n = RMSNorm(res) w_pre;  y = MoE(n);
+#   res_out = alpha res + beta gate * (RMSNorm(y) w_post or y)
+# and, where the next block's pre-norm weight is given, that block's n from the same pass.
+
+class BlockBuffers:
+    """Activations of one block: the layer's (``moe``, a MoEBuffers), the normed input
+    ``n``, the residual stream after the block ``res_out`` and the next block's input
+    ``n_next``; for training the gradients ``dres`` (of res), ``dy`` (of the layer's
+    output), ``dw_pre``, ``dw_post``, ``dw_next`` [d] and ``dgate``.
+
+    ``norm``: MoeNormCfg (eps, the factors alpha and beta, tokens per row of the gate).
+    ``res_dtype``: type of the residual stream, torch.bfloat16 or torch.float32."""
+
+    def __init__(self, dims: L.MoeDims, norm: L.MoeNormCfg, res_dtype=torch.bfloat16,
+                 device="cuda", train: bool = False, gather: bool = False, route=None):
+        self.dims, self.norm = dims, norm
+        self.moe = MoEBuffers(dims, device=device, train=train, gather=gather, route=route)
+        T, d = dims.T, dims.d
+        dev = torch.device(device)
+        e = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device=dev)
+        self.n, self.n_next = e(T, d), e(T, d)
+        self.res_out = e(T, d, dt=res_dtype)
+        if train:
+            f32 = torch.float32
+            rows = max(1, -(-T // norm.seq_len)) if norm.seq_len > 0 else 1
+            self.dy = e(T, d)
+            self.dres = e(T, d, dt=res_dtype)
+            self.dw_pre, self.dw_post, self.dw_next = (e(d, dt=f32) for _ in range(3))
+            self.dgate = e(rows, d, dt=f32)
+            self.ws = e(L.moe_norm_workspace_size(dims, norm), dt=torch.uint8)
+
+
+def block_forward(bb: BlockBuffers, res, w_pre, wg, bias, w1, w2, w_post=None, gate=None,
+                  w_next=None, n=None, stream=None, seq_balance=None):
+    """res_out (and the next block's input) of a block on the residual stream res [T, d].
+
+    w_pre [d] f32: the layer's pre-norm; with ``n`` [T, d] bf16, the normed input that the
+    block before returned, it is not used.  w_post [d] f32, gate [rows, d] f32: the norm
+    and the gate of the layer's output (None: without).  w_next [d] f32: the next block's
+    pre-norm.  Returns (res_out, n_next), n_next None without w_next."""
+    dm, cfg = bb.dims, bb.norm
+    if n is None:
+        n = bb.n
+        L.moe_block_norm(dm, cfg, None, res, None, None, w_pre, None, n, stream)
+    y = forward(bb.moe, n, wg, bias, w1, w2, stream=stream, seq_balance=seq_balance)
+    n_next = bb.n_next if w_next is not None else None
+    L.moe_block_norm(dm, cfg, y, res, w_post, gate, w_next, bb.res_out, n_next, stream)
+    return bb.res_out, n_next
+
+
+def block_backward(bb: BlockBuffers, dres_out, res, w_pre, wg, w1, w2, w_post=None, gate=None,
+                   w_next=None, n=None, dn_next=None, stream=None, gamma=None, bias=None):
+    """Gradients after ``block_forward`` with the same arguments.  dres_out [T, d]: of
+    res_out (None: zero, with w_next only); dn_next [T, d] bf16: of n_next, with w_next.
+
+    Returns dres [T, d], the gradient of res; where the block was given ``n``, (dres, dn):
+    the parts that reached res past the layer and n, for the block before.  Leaves the
+    weights' gradients in bb.dw_pre, bb.dw_post, bb.dw_next, bb.dgate and bb.moe."""
+    dm, cfg = bb.dims, bb.norm
+    if (w_next is None) != (dn_next is None):
+        raise ValueError("w_next and dn_next come together")
+    moe = bb.moe
+    L.moe_block_norm_bwd(dm, cfg, dn_next, dres_out, moe.out, bb.res_out, w_post, gate, w_next,
+                         bb.dy, bb.dres, bb.dw_post if w_post is not None else None,
+                         bb.dgate if gate is not None else None,
+                         bb.dw_next if w_next is not None else None, 0, bb.ws, stream)
+    dn, *_ = backward(moe, bb.n if n is None else n, bb.dy, w1, w2, stream=stream, wg=wg,
+                      gamma=gamma, bias=bias)
+    if n is not None:
+        return bb.dres, dn
+    L.moe_block_norm_bwd(dm, cfg, dn, bb.dres, None, res, None, None, w_pre, None, bb.dres, None,
+                         None, bb.dw_pre, 0, bb.ws, stream)
+    return bb.dres
+
+
 class HostPipeline:
     """Forward (+ backward) steps fed from and returned to pinned host memory,
     with the copies of neighbouring steps overlapped with compute.
@@ -220,13 +376,15 @@ class HostPipeline:
     """
 
     def __init__(self, dims: L.MoeDims, w1, w2, wg, bias, train: bool, device="cuda",
-                 gamma=None, graphs: bool = True, gather: bool = False, seq_balance=None):
+                 gamma=None, graphs: bool = True, gather: bool = False, seq_balance=None,
+                 route=None):
         self.dims, self.train, self.gamma = dims, train, gamma
         self.seq_balance = seq_balance if train else None
         self.w1, self.w2, self.wg, self.bias = w1, w2, wg, bias
         dev = torch.device(device)
         T, d = dims.T, dims.d
-        self.bufs = [MoEBuffers(dims, device=dev, train=train, gather=gather) for _ in range(2)]
+        self.bufs = [MoEBuffers(dims, device=dev, train=train, gather=gather, route=route)
+                     for _ in range(2)]
         # zero-filled: with graphs, one step runs on them before the capture
         e = lambda: torch.zeros(T, d, dtype=torch.bfloat16, device=dev)
         self.x = [e(), e()]

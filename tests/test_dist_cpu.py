@@ -227,3 +227,56 @@ def test_expert_parallel_plan_flags_an_owner_over_capacity():
     table = np.array([[100, 0, 300, 40], [5, 0, 200, 1]])
     for r in range(2):
         assert ep_plan_reference(table, r, 32, 600)["over"].tolist() == [0, 1]
+
+
+def _clip_worker(rank, world, port, q):
+    """layer.GradClip's order of calls and exchange, with the library's calls played by
+    torch on the host."""
+    os.environ.update(MASTER_ADDR="127.0.0.1", MASTER_PORT=str(port), RANK=str(rank),
+                      WORLD_SIZE=str(world), LOCAL_RANK=str(rank))
+    sys.path.insert(0, ROOT)
+    import torch
+    import torch.distributed as dist
+    from grouped_gemm_fp32_b200 import _lib, layer
+    dist.init_process_group("gloo", rank=rank, world_size=world)
+    _lib._types()["device"] = lambda: -1     # host tensors
+
+    def norm(lst, accumulate, sumsq, out, ws, stream=None):
+        v = sum(float(g.double().square().sum()) for g in lst.grads)
+        sumsq.copy_(sumsq + v if accumulate else torch.tensor([v], dtype=torch.float64))
+
+    def clip(lst, sumsq, max_norm, out, coef, stream=None):
+        f = min(1.0, max_norm / (float(sumsq.sqrt()) + 1e-6))
+        for g in lst.grads:
+            g.mul_(f)
+        if out is not None:
+            out.copy_(sumsq.sqrt())
+
+    _lib.moe_grad_norm, _lib.moe_grad_clip = norm, clip
+    _lib.moe_grad_workspace_size = lambda n: 256
+    shared = torch.full((5,), 2.0)                      # the same on every rank
+    mine = torch.full((3,), float(rank + 1))            # this rank's expert
+    c = layer.GradClip([shared], sharded=[mine])
+    got = float(c.clip(1.0)[0])
+    want = (5 * 4.0 + sum(3.0 * (r + 1) ** 2 for r in range(world))) ** 0.5
+    ok = abs(got - want) < 1e-5 * want
+    ok &= bool(torch.allclose(shared, torch.full((5,), 2.0 / want), rtol=1e-5))
+    ok &= bool(torch.allclose(mine, torch.full((3,), (rank + 1) / want), rtol=1e-5))
+    dist.barrier()
+    dist.destroy_process_group()
+    q.put((rank, ok))
+
+
+@pytest.mark.parametrize("world", [2, 3])
+def test_clipping_adds_the_ranks_shards_once(world):
+    ctx = mp.get_context("spawn")
+    q = ctx.Queue()
+    port = _free_port()
+    procs = [ctx.Process(target=_clip_worker, args=(r, world, port, q)) for r in range(world)]
+    for p in procs:
+        p.start()
+    out = [q.get(timeout=240) for _ in procs]
+    for p in procs:
+        p.join(timeout=60)
+        assert p.exitcode == 0
+    assert all(ok for _, ok in out)
