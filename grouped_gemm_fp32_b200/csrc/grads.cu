@@ -19,6 +19,7 @@ namespace moe {
 namespace {
 
 constexpr int GL_MAX = 512;      // tensors per launch
+constexpr int GL_FEW = 48;       // of a launch with the short table
 constexpr int GL_CTAS = 592;     // CTAs of a launch (four an SM); a norm launch's partial sums
 constexpr int GL_THREADS = 256;
 constexpr int GL_CHUNK = 16384;  // most elements of a chunk: 8 vectors a thread of bf16
@@ -31,9 +32,12 @@ struct GradEnt {
   int64_t chunk0;  // chunks of the launch's earlier tensors
 };
 
+// N: the most tensors of a launch.  The table is copied at every launch, so a list of few
+// tensors goes in a short one.
+template <int N>
 struct GradTable {
-  GradEnt e[GL_MAX];
-  uint8_t type[GL_MAX];
+  GradEnt e[N];
+  uint8_t type[N];
   int n;
   int chunk;       // elements of a chunk: less than GL_CHUNK where that fills more CTAs
   int64_t chunks;
@@ -47,7 +51,8 @@ __device__ __forceinline__ void from_f32(__nv_bfloat16* p, float v) { *p = __flo
 __device__ __forceinline__ void from_f32(__half* p, float v) { *p = __float2half_rn(v); }
 
 // The tensor that holds a chunk: the last one whose first chunk is not past it.
-__device__ __forceinline__ int find(const GradTable& tb, int64_t chunk) {
+template <int N>
+__device__ __forceinline__ int find(const GradTable<N>& tb, int64_t chunk) {
   int lo = 0, hi = tb.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -131,8 +136,9 @@ __device__ double block_sum(double v) {
   return v;
 }
 
+template <int N>
 __global__ void __launch_bounds__(GL_THREADS, 4)
-    grad_sumsq_kernel(const __grid_constant__ GradTable tb, double* __restrict__ part) {
+    grad_sumsq_kernel(const __grid_constant__ GradTable<N> tb, double* __restrict__ part) {
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
   for (int64_t c = blockIdx.x; c < tb.chunks; c += gridDim.x) {
     const int k = find(tb, c);
@@ -252,8 +258,9 @@ __device__ void chunk_scale(const void* data, void* out, int64_t i0, int64_t i1,
 // parts > 0: the sum of squares is that of the norm launches' partial sums, which every
 // CTA adds up for itself, and is written to sumsq; otherwise sumsq is given.  The chunks
 // are taken in the reverse of the norm's order: what it read last may still be in the L2.
+template <int N>
 __global__ void __launch_bounds__(GL_THREADS, 4)
-    grad_clip_kernel(const __grid_constant__ GradTable tb, const double* part, int64_t parts,
+    grad_clip_kernel(const __grid_constant__ GradTable<N> tb, const double* part, int64_t parts,
                      double* sumsq, float max_norm, float* norm, float* coef) {
   cudaGridDependencySynchronize();  // launched while the norm's last CTAs still ran
   const double ss = parts > 0 ? sum_parts(part, parts) : *sumsq;
@@ -279,10 +286,11 @@ __global__ void __launch_bounds__(GL_THREADS, 4)
 }
 
 // The next launch's table: tensors from *i on, empty ones left out.
-void fill(GradTable& tb, const moe_grad* g, int64_t n, int64_t* i) {
+template <int N>
+void fill(GradTable<N>& tb, const moe_grad* g, int64_t n, int64_t* i) {
   tb.n = 0;
   int64_t total = 0;
-  for (; *i < n && tb.n < GL_MAX; ++*i) {
+  for (; *i < n && tb.n < N; ++*i) {
     const moe_grad& x = g[*i];
     if (x.n == 0) continue;
     GradEnt& e = tb.e[tb.n];
@@ -310,17 +318,21 @@ size_t grad_ws_bytes(int64_t n) {
 }
 
 // The norm's launches over a list; returns how many partial sums they leave in part.
-static int64_t sumsq_launches(const moe_grad* g, int64_t n, double* part, cudaStream_t st) {
+template <int N>
+static int64_t sumsq_with(const moe_grad* g, int64_t n, double* part, cudaStream_t st) {
   int64_t parts = 0;
   for (int64_t i = 0; i < n;) {
-    GradTable tb;
+    GradTable<N> tb;
     fill(tb, g, n, &i);
     if (tb.n == 0) break;
     const unsigned ctas = (unsigned)(tb.chunks < GL_CTAS ? tb.chunks : GL_CTAS);
-    grad_sumsq_kernel<<<ctas, GL_THREADS, 0, st>>>(tb, part + parts);
+    grad_sumsq_kernel<N><<<ctas, GL_THREADS, 0, st>>>(tb, part + parts);
     parts += ctas;
   }
   return parts;
+}
+static int64_t sumsq_launches(const moe_grad* g, int64_t n, double* part, cudaStream_t st) {
+  return n <= GL_FEW ? sumsq_with<GL_FEW>(g, n, part, st) : sumsq_with<GL_MAX>(g, n, part, st);
 }
 
 int launch_grad_norm(const moe_grad* g, int64_t n, int accumulate, double* sumsq, float* norm,
@@ -334,13 +346,13 @@ int launch_grad_norm(const moe_grad* g, int64_t n, int accumulate, double* sumsq
 
 // The clipping's launches, last tensors first.  parts > 0: after the norm's, by its
 // partial sums.
-static int clip_launches(const moe_grad* g, int64_t n, const double* part, int64_t parts,
-                         double* sumsq, float max_norm, float* norm, float* coef,
-                         cudaStream_t st) {
+template <int N>
+static int clip_with(const moe_grad* g, int64_t n, const double* part, int64_t parts,
+                     double* sumsq, float max_norm, float* norm, float* coef, cudaStream_t st) {
   bool first = true;
   int64_t i = 0;
   do {
-    GradTable tb;
+    GradTable<N> tb;
     fill(tb, g, n, &i);
     const int64_t ctas = tb.chunks < GL_CTAS ? (tb.chunks > 0 ? tb.chunks : 1) : GL_CTAS;
     cudaLaunchConfig_t cfg = {};
@@ -352,12 +364,18 @@ static int clip_launches(const moe_grad* g, int64_t n, const double* part, int64
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = parts > 0 && first ? 1 : 0;  // directly behind a launch of the norm's
-    if (!cuda_ok(cudaLaunchKernelEx(&cfg, grad_clip_kernel, tb, part, parts, sumsq, max_norm,
+    if (!cuda_ok(cudaLaunchKernelEx(&cfg, grad_clip_kernel<N>, tb, part, parts, sumsq, max_norm,
                                     norm, coef)))
       return MOE_ERR_CUDA;
     first = false;
   } while (i < n);
   return MOE_OK;
+}
+static int clip_launches(const moe_grad* g, int64_t n, const double* part, int64_t parts,
+                         double* sumsq, float max_norm, float* norm, float* coef,
+                         cudaStream_t st) {
+  return n <= GL_FEW ? clip_with<GL_FEW>(g, n, part, parts, sumsq, max_norm, norm, coef, st)
+                     : clip_with<GL_MAX>(g, n, part, parts, sumsq, max_norm, norm, coef, st);
 }
 
 int launch_grad_clip(const moe_grad* g, int64_t n, const double* sumsq, float max_norm,

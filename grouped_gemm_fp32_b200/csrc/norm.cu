@@ -558,6 +558,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
       flushed = true;
     }
   }
+  cudaTriggerProgrammaticLaunchCompletion();  // block_norm_bwd_finish may come in
   if (a.pre)
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -572,25 +573,27 @@ struct FinK {
   float beta;
 };
 
-// Column sums of the CTAs' rows: job 0 dw_post, 1 dw_pre, 2 + s dgate row s.
-// 32 columns x 8 strands of rows, the strands added in order.
+// Column sums of the CTAs' rows: job 0 dw_post, 1 dw_pre, 2 + s dgate row s.  A CTA takes
+// 32 columns (d is a multiple of 64), four a thread, and 32 strands of rows, which are added
+// in a fixed order.  Launched while the sums' CTAs leave, and bound by latency: a strand has
+// some nine rows, all on their way at once.
 __global__ void __launch_bounds__(256) block_norm_bwd_finish(const FinK a) {
-  __shared__ float sh[8][32];
-  const int x = threadIdx.x & 31, strand = threadIdx.x >> 5;
-  const int cols = (a.d + 31) / 32;
+  __shared__ float4 sh[8][8];
+  const int x = threadIdx.x & 7, strand = threadIdx.x >> 3;
+  const int cols = a.d / 32;
   const int64_t job = blockIdx.x / cols;
-  const int c = (int)(blockIdx.x - job * cols) * 32 + x;
+  const int c = (int)(blockIdx.x - job * cols) * 32 + x * 4;
   const float* src;
   float* dst;
   int64_t r0 = 0, r1 = a.ctas;
-  float f = 1.0f;
+  float4 f = make_float4(a.beta, a.beta, a.beta, a.beta);
   if (job == 0) {
     src = a.post;
     dst = a.dw_post;
-    f = a.beta;
   } else if (job == 1) {
     src = a.pre;
     dst = a.dw_pre;
+    f = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
   } else {
     const int64_t s = job - 2;
     const int64_t last = min((s + 1) * a.seq_len, a.T) - 1;
@@ -598,17 +601,36 @@ __global__ void __launch_bounds__(256) block_norm_bwd_finish(const FinK a) {
     r1 = last / a.rows + s + 1;
     src = a.seq;
     dst = a.dgate ? a.dgate + s * a.d : nullptr;
-    f = a.beta * (a.w_post && c < a.d ? a.w_post[c] : 1.0f);
+    if (a.w_post) {
+      const float4 w = *reinterpret_cast<const float4*>(a.w_post + c);
+      f = make_float4(f.x * w.x, f.y * w.y, f.z * w.z, f.w * w.w);
+    }
   }
   if (dst == nullptr) return;
-  float v = 0.0f;
-  if (c < a.d)
-    for (int64_t r = r0 + strand; r < r1; r += 8) v += src[r * a.d + c];
-  sh[strand][x] = v;
+  cudaGridDependencySynchronize();
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [](float4& p, const float4& q) {
+    p.x += q.x;
+    p.y += q.y;
+    p.z += q.z;
+    p.w += q.w;
+  };
+  src += c;
+#pragma unroll 10
+  for (int64_t r = r0 + strand; r < r1; r += 32)
+    add(v, *reinterpret_cast<const float4*>(src + r * a.d));
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1)
+    add(v, make_float4(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o),
+                       __shfl_xor_sync(0xffffffffu, v.z, o), __shfl_xor_sync(0xffffffffu, v.w, o)));
+  if ((strand & 3) == 0) sh[strand >> 2][x] = v;
   __syncthreads();
-  if (strand == 0 && c < a.d) {
-    for (int i = 1; i < 8; ++i) v += sh[i][x];
-    dst[c] = a.accumulate ? dst[c] + f * v : f * v;
+  if (strand == 0) {
+    for (int i = 1; i < 8; ++i) add(v, sh[i][x]);
+    float4* p = reinterpret_cast<float4*>(dst + c);
+    float4 o = make_float4(f.x * v.x, f.y * v.y, f.z * v.z, f.w * v.w);
+    if (a.accumulate) add(o, *p);
+    *p = o;
   }
 }
 
@@ -725,7 +747,7 @@ int launch_block_norm_bwd(const moe_dims& dm, const moe_norm_cfg& c, int res_typ
                           const NormArgs& a, void* stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t seqs = gate_rows(dm, c);
-  if ((2 + seqs) * ((dm.d + 31) / 32) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if ((2 + seqs) * (dm.d / 32) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
   BwdK k{};
   k.dn = reinterpret_cast<const __nv_bfloat16*>(a.dn);
   k.y = reinterpret_cast<const __nv_bfloat16*>(a.y);
@@ -768,8 +790,16 @@ int launch_block_norm_bwd(const moe_dims& dm, const moe_norm_cfg& c, int res_typ
   f.d = dm.d;
   f.accumulate = a.accumulate;
   f.beta = a.y ? c.block_scale : 1.0f;
-  block_norm_bwd_finish<<<(unsigned)((2 + seqs) * ((dm.d + 31) / 32)), 256, 0, st>>>(f);
-  return cuda_ok(cudaGetLastError()) ? MOE_OK : MOE_ERR_CUDA;
+  cudaLaunchConfig_t launch = {};
+  launch.gridDim = dim3((unsigned)((2 + seqs) * (dm.d / 32)));
+  launch.blockDim = dim3(256);
+  launch.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  launch.attrs = attr;
+  launch.numAttrs = ctas ? 1 : 0;  // directly behind the sums' launch
+  return cuda_ok(cudaLaunchKernelEx(&launch, block_norm_bwd_finish, f)) ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace moe
