@@ -385,41 +385,65 @@ def grouped_gemm_bwd_dx_ep(dims, ws, peers, which, dy_recv, dy_shared, w, a1, ou
 # ---------------------------------------------------- routers of other kinds --
 # The calls below read a tensor's element type from its dtype, so they check what
 # they are given: dtype, element count, contiguity and that the tensor is on the
-# current device.  Integer addresses pass unchecked, as in the calls above.
+# current device.  Integer addresses pass unchecked, as in the calls above.  They are
+# called often and on little data, so csrc/bind.cpp does the checks and the C call; what
+# does not pass there comes back to _need and _kind, which say what is wrong.
 _TYPES: dict = {}
+_bound = None
 
 
 def _types():
     if not _TYPES:
         import torch
         _TYPES.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16})
-        _TYPES.update(f32=torch.float32, i32=torch.int32, bf16=torch.bfloat16, u8=torch.uint8,
-                      f64=torch.float64, device=torch.cuda.current_device)
         # the same numbers without a Stream object and the lazy start of CUDA on the way
-        # (1.5 us less a call); a torch without the call keeps to the public ones
+        # (3 us less a call); a torch without the call keeps to the public one
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _TYPES["stream"] = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        _TYPES.update(device=torch.cuda.current_device,
+                      stream=raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
     return _TYPES
 
 
-def _here(stream, dev):
-    """As _s, on the current device ``dev``."""
-    return _types()["stream"](dev) if stream is None else _s(stream)
+def _bind():
+    """csrc/bind.cpp's calls, on the library that load() gives."""
+    global _bound
+    if _bound is None:
+        import torch
+        lib = load()
+        try:
+            from . import _bind as b
+        except ImportError as e:
+            raise ImportError(f"{_HERE}/_bind.so: {e}; build it with "
+                              "`python -m grouped_gemm_fp32_b200.build` (there is no fallback)")
+        _types()
+        b.start(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "moe_gate_logits", "moe_route_topk", "moe_route_bwd", "moe_gate_bwd",
+            "moe_block_norm", "moe_block_norm_bwd", "moe_grad_norm", "moe_grad_clip",
+            "moe_grad_clip_norm")), _need, _kind,
+            (torch.float32, torch.bfloat16, torch.float16, torch.int32, torch.float64))
+        _bound = b
+    return _bound
+
+
+def _here(stream):
+    """The current device, and a stream on it as _s gives it."""
+    dev = _types()["device"]()
+    return dev, _TYPES["stream"](dev) if stream is None else _s(stream)
 
 
 def _need(what, t, dtype, numel, dev):
     """Device pointer of a tensor after its checks; NULL for None."""
     if t is None or type(t) is int:
         return t
-    if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and t.get_device() == dev:
-        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{what}: {t.dtype} given, {dtype} needed")
     if t.numel() != numel:
         raise ValueError(f"{what}: shape {tuple(t.shape)} has {t.numel()} elements, {numel} needed")
     if not t.is_contiguous():
         raise ValueError(f"{what}: not contiguous (strides {t.stride()})")
-    raise ValueError(f"{what}: on {t.device}, the current device is cuda:{dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, the current device is cuda:{dev}")
+    return t.data_ptr()
 
 
 def _kind(what, t, allowed):
@@ -430,86 +454,32 @@ def _kind(what, t, allowed):
     return ty
 
 
-def _bytes(what, ws, dev):
-    if ws.get_device() != dev or not ws.is_contiguous():
-        raise ValueError(f"{what}: a contiguous tensor on cuda:{dev} is needed")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
-
-
 def moe_gate_logits(dims, x, wg, logits, ws, stream=None):
-    y = _types()
-    dev = y["device"]()
-    T, d, E = dims.T, dims.d, dims.E
-    _ck(load().moe_gate_logits(ctypes.byref(dims), _need("x", x, y["bf16"], T * d, dev),
-                               _need("wg", wg, y["f32"], E * d, dev),
-                               _need("logits", logits, y["f32"], T * E, dev),
-                               *_bytes("ws", ws, dev), _here(stream, dev)), "moe_gate_logits")
+    _ck((_bound or _bind()).gate_logits(dims, x, wg, logits, ws, *_here(stream)),
+        "moe_gate_logits")
 
 
 def moe_route_topk(dims, cfg, logits, bias, topk_idx, topk_w, probs, stream=None):
-    y = _types()
-    dev, f32 = y["device"](), y["f32"]
-    T, E, k = dims.T, dims.E, dims.k
-    kind = _kind("logits", logits, (MOE_F32, MOE_BF16))
-    _ck(load().moe_route_topk(ctypes.byref(dims), ctypes.byref(cfg), kind,
-                              _need("logits", logits, logits.dtype, T * E, dev),
-                              _need("bias", bias, f32, E, dev),
-                              _need("topk_idx", topk_idx, y["i32"], T * k, dev),
-                              _need("topk_w", topk_w, f32, T * k, dev),
-                              _need("probs", probs, f32, T * E, dev), _here(stream, dev)),
-        "moe_route_topk")
+    _ck((_bound or _bind()).route_topk(dims, cfg, logits, bias, topk_idx, topk_w, probs,
+                                       *_here(stream)), "moe_route_topk")
 
 
 def moe_route_bwd(dims, cfg, logits, topk_idx, topk_w, dw, seq_grad, seq_len, dlogits,
                   stream=None):
-    y = _types()
-    dev, f32 = y["device"](), y["f32"]
-    T, E, k = dims.T, dims.E, dims.k
-    kind = _kind("logits", logits, (MOE_F32, MOE_BF16))
-    seq_len = int(seq_len)
-    rows = -(-T // seq_len) if seq_grad is not None and seq_len > 0 else 0
-    if rows and type(seq_grad) is not int and seq_grad.numel() > rows * E:
-        seq_grad = seq_grad.view(-1)[:rows * E]     # MoEBuffers.bal_grad holds more rows
-    _ck(load().moe_route_bwd(ctypes.byref(dims), ctypes.byref(cfg), kind,
-                             _need("logits", logits, logits.dtype, T * E, dev),
-                             _need("topk_idx", topk_idx, y["i32"], T * k, dev),
-                             _need("topk_w", topk_w, f32, T * k, dev),
-                             _need("dw", dw, f32, T * k, dev),
-                             _need("seq_grad", seq_grad, f32, rows * E, dev), seq_len,
-                             _need("dlogits", dlogits, logits.dtype, T * E, dev),
-                             _here(stream, dev)),
-        "moe_route_bwd")
+    # seq_grad may have more rows than the call's sequences (MoEBuffers.bal_grad has)
+    _ck((_bound or _bind()).route_bwd(dims, cfg, logits, topk_idx, topk_w, dw, seq_grad, seq_len,
+                                      dlogits, *_here(stream)), "moe_route_bwd")
 
 
 def moe_gate_bwd(dims, x, wg, dlogits, dx, dwg, accumulate, ws, stream=None):
-    y = _types()
-    dev, f32 = y["device"](), y["f32"]
-    T, d, E = dims.T, dims.d, dims.E
-    _ck(load().moe_gate_bwd(ctypes.byref(dims), _need("x", x, y["bf16"], T * d, dev),
-                            _need("wg", wg, f32, E * d, dev),
-                            _need("dlogits", dlogits, f32, T * E, dev),
-                            _need("dx", dx, y["bf16"], T * d, dev),
-                            _need("dwg", dwg, f32, E * d, dev), int(accumulate),
-                            *_bytes("ws", ws, dev), _here(stream, dev)), "moe_gate_bwd")
+    _ck((_bound or _bind()).gate_bwd(dims, x, wg, dlogits, dx, dwg, accumulate, ws,
+                                     *_here(stream)), "moe_gate_bwd")
 
 
 # ------------------------------------------------------------- block norms --
-def _gate_rows(dims, cfg) -> int:
-    return max(1, -(-dims.T // cfg.seq_len)) if cfg.seq_len > 0 else 1
-
-
 def moe_block_norm(dims, cfg, y, res, w_post, gate, w_pre, res_out, n, stream=None):
-    ty = _types()
-    dev, f32, bf = ty["device"](), ty["f32"], ty["bf16"]
-    d, m = dims.d, dims.T * dims.d
-    kind = _kind("res", res, (MOE_F32, MOE_BF16))
-    _ck(load().moe_block_norm(ctypes.byref(dims), ctypes.byref(cfg), kind,
-                              _need("y", y, bf, m, dev), _need("res", res, res.dtype, m, dev),
-                              _need("w_post", w_post, f32, d, dev),
-                              _need("gate", gate, f32, _gate_rows(dims, cfg) * d, dev),
-                              _need("w_pre", w_pre, f32, d, dev),
-                              _need("res_out", res_out, res.dtype, m, dev),
-                              _need("n", n, bf, m, dev), _here(stream, dev)), "moe_block_norm")
+    _ck((_bound or _bind()).block_norm(dims, cfg, y, res, w_post, gate, w_pre, res_out, n,
+                                       *_here(stream)), "moe_block_norm")
 
 
 def moe_norm_workspace_size(dims, cfg) -> int:
@@ -518,23 +488,9 @@ def moe_norm_workspace_size(dims, cfg) -> int:
 
 def moe_block_norm_bwd(dims, cfg, dn, dres_out, y, u, w_post, gate, w_pre, dy, dres, dw_post,
                        dgate, dw_pre, accumulate, ws, stream=None):
-    ty = _types()
-    dev, f32, bf = ty["device"](), ty["f32"], ty["bf16"]
-    d, m, g = dims.d, dims.T * dims.d, _gate_rows(dims, cfg) * dims.d
-    kind = _kind("dres", dres, (MOE_F32, MOE_BF16))
-    rt = dres.dtype
-    _ck(load().moe_block_norm_bwd(ctypes.byref(dims), ctypes.byref(cfg), kind,
-                                  _need("dn", dn, bf, m, dev),
-                                  _need("dres_out", dres_out, rt, m, dev),
-                                  _need("y", y, bf, m, dev), _need("u", u, rt, m, dev),
-                                  _need("w_post", w_post, f32, d, dev),
-                                  _need("gate", gate, f32, g, dev),
-                                  _need("w_pre", w_pre, f32, d, dev), _need("dy", dy, bf, m, dev),
-                                  _need("dres", dres, rt, m, dev),
-                                  _need("dw_post", dw_post, f32, d, dev),
-                                  _need("dgate", dgate, f32, g, dev),
-                                  _need("dw_pre", dw_pre, f32, d, dev), int(accumulate),
-                                  *_bytes("ws", ws, dev), _here(stream, dev)), "moe_block_norm_bwd")
+    _ck((_bound or _bind()).block_norm_bwd(dims, cfg, dn, dres_out, y, u, w_post, gate, w_pre, dy,
+                                           dres, dw_post, dgate, dw_pre, accumulate, ws,
+                                           *_here(stream)), "moe_block_norm_bwd")
 
 
 # ---------------------------------------------------------- gradient clipping --
@@ -549,6 +505,7 @@ class GradList:
         if len(self.outs) != len(self.grads):
             raise ValueError(f"{len(self.grads)} gradients, {len(self.outs)} outs")
         self.array = (MoeGrad * max(1, len(self.grads)))()
+        self.address = ctypes.addressof(self.array)
         dev = _types()["device"]() if self.grads else 0
         for a, g, o in zip(self.array, self.grads, self.outs):
             a.type = _kind("gradient", g, (MOE_F32, MOE_BF16, MOE_F16))
@@ -565,29 +522,15 @@ def moe_grad_workspace_size(n_grads) -> int:
 
 
 def moe_grad_norm(grads, accumulate, sumsq, norm, ws, stream=None):
-    y = _types()
-    dev = y["device"]()
-    _ck(load().moe_grad_norm(ctypes.addressof(grads.array), len(grads), int(accumulate),
-                             _need("sumsq", sumsq, y["f64"], 1, dev),
-                             _need("norm", norm, y["f32"], 1, dev), *_bytes("ws", ws, dev),
-                             _here(stream, dev)), "moe_grad_norm")
+    _ck((_bound or _bind()).grad_norm(grads.address, len(grads), accumulate, sumsq, norm, ws,
+                                      *_here(stream)), "moe_grad_norm")
 
 
 def moe_grad_clip(grads, sumsq, max_norm, norm, coef, stream=None):
-    y = _types()
-    dev = y["device"]()
-    _ck(load().moe_grad_clip(ctypes.addressof(grads.array), len(grads),
-                             _need("sumsq", sumsq, y["f64"], 1, dev), float(max_norm),
-                             _need("norm", norm, y["f32"], 1, dev),
-                             _need("coef", coef, y["f32"], 1, dev), _here(stream, dev)),
-        "moe_grad_clip")
+    _ck((_bound or _bind()).grad_clip(grads.address, len(grads), sumsq, max_norm, norm, coef,
+                                      *_here(stream)), "moe_grad_clip")
 
 
 def moe_grad_clip_norm(grads, max_norm, sumsq, norm, coef, ws, stream=None):
-    y = _types()
-    dev = y["device"]()
-    _ck(load().moe_grad_clip_norm(ctypes.addressof(grads.array), len(grads), float(max_norm),
-                                  _need("sumsq", sumsq, y["f64"], 1, dev),
-                                  _need("norm", norm, y["f32"], 1, dev),
-                                  _need("coef", coef, y["f32"], 1, dev), *_bytes("ws", ws, dev),
-                                  _here(stream, dev)), "moe_grad_clip_norm")
+    _ck((_bound or _bind()).grad_clip_norm(grads.address, len(grads), max_norm, sumsq, norm, coef,
+                                           ws, *_here(stream)), "moe_grad_clip_norm")

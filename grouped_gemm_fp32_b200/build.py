@@ -1,7 +1,8 @@
 """Build ``libmoe.so`` (the C-ABI CUDA library) in-tree with nvcc for sm_100a, and
 ``libmoe_debug.so``, the same sources with MOE_DEBUG=1 (device-side checks of the
 group table and tile coordinates that report MOE_ERR_BAD_ROUTING instead of
-following a bad entry; loaded instead of libmoe.so when MOE_LIB_DEBUG=1).
+following a bad entry; loaded instead of libmoe.so when MOE_LIB_DEBUG=1), and with g++
+``_bind.so``, the Python calls of the operators around the layer (csrc/bind.cpp).
 
     python -m grouped_gemm_fp32_b200.build [--force]
 """
@@ -15,6 +16,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe.so")
+BIND = os.path.join(HERE, "_bind.so")
 LIB_DEBUG = os.path.join(HERE, "libmoe_debug.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
@@ -60,8 +62,31 @@ def _build_one(lib: str, extra, force: bool, verbose: bool):
     os.replace(tmp, lib)
 
 
+def _build_bind(force: bool, verbose: bool):
+    src, header = os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "moe.h")
+    newest = max(map(os.path.getmtime, (src, header, os.path.abspath(__file__))))
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= newest:
+        return
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           src, "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BIND)
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = True) -> str:
-    """Both libraries (the debug one unless ``debug`` is False); returns libmoe.so's path."""
+    """Both libraries (the debug one unless ``debug`` is False) and the binding; returns
+    libmoe.so's path."""
+    _build_bind(force, verbose)
     _build_one(LIB, [], force, verbose)
     if debug:
         _build_one(LIB_DEBUG, ["-DMOE_DEBUG=1"], force, verbose)
