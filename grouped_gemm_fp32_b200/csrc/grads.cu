@@ -139,6 +139,7 @@ __device__ double block_sum(double v) {
 template <int N>
 __global__ void __launch_bounds__(GL_THREADS, 4)
     grad_sumsq_kernel(const __grid_constant__ GradTable<N> tb, double* __restrict__ part) {
+  behind();
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
   for (int64_t c = blockIdx.x; c < tb.chunks; c += gridDim.x) {
     const int k = find(tb, c);
@@ -148,7 +149,6 @@ __global__ void __launch_bounds__(GL_THREADS, 4)
     else if (tb.type[k] == MOE_BF16) chunk_sum<__nv_bfloat16>(acc, tb.e[k].data, i0, i1);
     else chunk_sum<__half>(acc, tb.e[k].data, i0, i1);
   }
-  cudaTriggerProgrammaticLaunchCompletion();  // the clipping's CTAs may come in as these leave
   const double s = block_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
@@ -162,6 +162,7 @@ __device__ __forceinline__ double sum_parts(const double* part, int64_t n) {
 
 __global__ void __launch_bounds__(GL_THREADS)
     grad_finish_kernel(const double* part, int64_t n, int accumulate, double* sumsq, float* norm) {
+  behind();
   double s = sum_parts(part, n);
   if (threadIdx.x == 0) {
     if (accumulate) s += *sumsq;
@@ -262,7 +263,7 @@ template <int N>
 __global__ void __launch_bounds__(GL_THREADS, 4)
     grad_clip_kernel(const __grid_constant__ GradTable<N> tb, const double* part, int64_t parts,
                      double* sumsq, float max_norm, float* norm, float* coef) {
-  cudaGridDependencySynchronize();  // launched while the norm's last CTAs still ran
+  behind();
   const double ss = parts > 0 ? sum_parts(part, parts) : *sumsq;
   const double nm = sqrt(ss);
   const double q = (double)max_norm / (nm + 1e-6);
@@ -319,29 +320,35 @@ size_t grad_ws_bytes(int64_t n) {
 
 // The norm's launches over a list; returns how many partial sums they leave in part.
 template <int N>
-static int64_t sumsq_with(const moe_grad* g, int64_t n, double* part, cudaStream_t st) {
-  int64_t parts = 0;
+static int sumsq_with(const moe_grad* g, int64_t n, double* part, int64_t* parts,
+                      cudaStream_t st) {
+  *parts = 0;
   for (int64_t i = 0; i < n;) {
     GradTable<N> tb;
     fill(tb, g, n, &i);
     if (tb.n == 0) break;
-    const unsigned ctas = (unsigned)(tb.chunks < GL_CTAS ? tb.chunks : GL_CTAS);
-    grad_sumsq_kernel<N><<<ctas, GL_THREADS, 0, st>>>(tb, part + parts);
-    parts += ctas;
+    const int64_t ctas = tb.chunks < GL_CTAS ? tb.chunks : GL_CTAS;
+    const int rc = launch_behind(grad_sumsq_kernel<N>, ctas, GL_THREADS, 0, st, tb, part + *parts);
+    if (rc != MOE_OK) return rc;
+    *parts += ctas;
   }
-  return parts;
+  return MOE_OK;
 }
-static int64_t sumsq_launches(const moe_grad* g, int64_t n, double* part, cudaStream_t st) {
-  return n <= GL_FEW ? sumsq_with<GL_FEW>(g, n, part, st) : sumsq_with<GL_MAX>(g, n, part, st);
+static int sumsq_launches(const moe_grad* g, int64_t n, double* part, int64_t* parts,
+                          cudaStream_t st) {
+  return n <= GL_FEW ? sumsq_with<GL_FEW>(g, n, part, parts, st)
+                     : sumsq_with<GL_MAX>(g, n, part, parts, st);
 }
 
 int launch_grad_norm(const moe_grad* g, int64_t n, int accumulate, double* sumsq, float* norm,
                      void* ws, void* stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   double* part = reinterpret_cast<double*>(ws);
-  const int64_t parts = sumsq_launches(g, n, part, st);
-  grad_finish_kernel<<<1, GL_THREADS, 0, st>>>(part, parts, accumulate, sumsq, norm);
-  return cuda_ok(cudaGetLastError()) ? MOE_OK : MOE_ERR_CUDA;
+  int64_t parts;
+  const int rc = sumsq_launches(g, n, part, &parts, st);
+  if (rc != MOE_OK) return rc;
+  return launch_behind(grad_finish_kernel, 1, GL_THREADS, 0, st, part, parts, accumulate, sumsq,
+                       norm);
 }
 
 // The clipping's launches, last tensors first.  parts > 0: after the norm's, by its
@@ -349,25 +356,14 @@ int launch_grad_norm(const moe_grad* g, int64_t n, int accumulate, double* sumsq
 template <int N>
 static int clip_with(const moe_grad* g, int64_t n, const double* part, int64_t parts,
                      double* sumsq, float max_norm, float* norm, float* coef, cudaStream_t st) {
-  bool first = true;
   int64_t i = 0;
   do {
     GradTable<N> tb;
     fill(tb, g, n, &i);
     const int64_t ctas = tb.chunks < GL_CTAS ? (tb.chunks > 0 ? tb.chunks : 1) : GL_CTAS;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(GL_THREADS);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = parts > 0 && first ? 1 : 0;  // directly behind a launch of the norm's
-    if (!cuda_ok(cudaLaunchKernelEx(&cfg, grad_clip_kernel<N>, tb, part, parts, sumsq, max_norm,
-                                    norm, coef)))
-      return MOE_ERR_CUDA;
-    first = false;
+    const int rc = launch_behind(grad_clip_kernel<N>, ctas, GL_THREADS, 0, st, tb, part, parts,
+                                 sumsq, max_norm, norm, coef);
+    if (rc != MOE_OK) return rc;
   } while (i < n);
   return MOE_OK;
 }
@@ -388,8 +384,9 @@ int launch_grad_clip_norm(const moe_grad* g, int64_t n, float max_norm, double* 
                           float* norm, float* coef, void* ws, void* stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   double* part = reinterpret_cast<double*>(ws);
-  const int64_t parts = sumsq_launches(g, n, part, st);
-  if (!cuda_ok(cudaGetLastError())) return MOE_ERR_CUDA;
+  int64_t parts;
+  const int rc = sumsq_launches(g, n, part, &parts, st);
+  if (rc != MOE_OK) return rc;
   if (parts == 0 && !cuda_ok(cudaMemsetAsync(sumsq, 0, sizeof(double), st))) return MOE_ERR_CUDA;
   return clip_launches(g, n, part, parts, sumsq, max_norm, norm, coef, st);
 }

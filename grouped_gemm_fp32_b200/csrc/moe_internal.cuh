@@ -3,6 +3,7 @@
 #pragma once
 #include <cstddef>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -21,6 +22,31 @@ namespace moe {
 
 // Records the error of a failing CUDA call for moe_last_cuda_error(); true on success.
 bool cuda_ok(cudaError_t e);
+
+// Launches a kernel that may come in while the stream's last kernel leaves (one to two
+// microseconds less between two small launches).  Such a kernel begins with behind(), before
+// it touches any memory, and so waits for everything before it all the same.
+template <typename... P>
+int launch_behind(void (*kernel)(P...), int64_t ctas, int threads, size_t smem, cudaStream_t st,
+                  const std::common_type_t<P>&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, kernel, args...)) ? MOE_OK : MOE_ERR_CUDA;
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void behind() {
+  cudaTriggerProgrammaticLaunchCompletion();  // the next one's CTAs may come in
+  cudaGridDependencySynchronize();            // the last one's work is done and visible
+}
+#endif
 
 // Argument and shape checks every entry point runs first (moe_api.cu): dims_ok
 // is false for a null or non-positive shape; check_shape returns

@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(cons
   constexpr int R = sizeof(RT) / 2, H = NV / 2;
   extern __shared__ uint4 ring[];
   __shared__ __align__(16) float sh[2 * MAX_WARPS];
+  behind();
   int half = 0;
   const int nvec = a.d / NV, tid = threadIdx.x, nt = blockDim.x;
   const int64_t t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
@@ -383,6 +384,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
   constexpr int R = sizeof(RT) / 2, H = NV / 2;
   extern __shared__ uint4 ring[];
   __shared__ float sh[2 * MAX_WARPS * 8];
+  behind();
   int half = 0;
   const int nvec = a.d / NV, tid = threadIdx.x, nt = blockDim.x;
   const int64_t t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
@@ -558,7 +560,6 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
       flushed = true;
     }
   }
-  cudaTriggerProgrammaticLaunchCompletion();  // block_norm_bwd_finish may come in
   if (a.pre)
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -575,10 +576,11 @@ struct FinK {
 
 // Column sums of the CTAs' rows: job 0 dw_post, 1 dw_pre, 2 + s dgate row s.  A CTA takes
 // 32 columns (d is a multiple of 64), four a thread, and 32 strands of rows, which are added
-// in a fixed order.  Launched while the sums' CTAs leave, and bound by latency: a strand has
+// in a fixed order.  Bound by latency: a strand has
 // some nine rows, all on their way at once.
 __global__ void __launch_bounds__(256) block_norm_bwd_finish(const FinK a) {
   __shared__ float4 sh[8][8];
+  behind();
   const int x = threadIdx.x & 7, strand = threadIdx.x >> 3;
   const int cols = a.d / 32;
   const int64_t job = blockIdx.x / cols;
@@ -607,7 +609,6 @@ __global__ void __launch_bounds__(256) block_norm_bwd_finish(const FinK a) {
     }
   }
   if (dst == nullptr) return;
-  cudaGridDependencySynchronize();
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   auto add = [](float4& p, const float4& q) {
     p.x += q.x;
@@ -673,8 +674,7 @@ int launch_rows(void (*kernel)(const K), std::atomic<uint64_t>& ready, K k, int 
   k.stages = (int)n;
   const int bytes = (int)(n * stage);
   if (!opt_in(kernel, ready)) return MOE_ERR_CUDA;
-  kernel<<<(unsigned)ctas, s.threads, bytes, st>>>(k);
-  return cuda_ok(cudaGetLastError()) ? MOE_OK : MOE_ERR_CUDA;
+  return launch_behind(kernel, ctas, s.threads, bytes, st, k);
 }
 
 template <typename RT>
@@ -790,16 +790,7 @@ int launch_block_norm_bwd(const moe_dims& dm, const moe_norm_cfg& c, int res_typ
   f.d = dm.d;
   f.accumulate = a.accumulate;
   f.beta = a.y ? c.block_scale : 1.0f;
-  cudaLaunchConfig_t launch = {};
-  launch.gridDim = dim3((unsigned)((2 + seqs) * (dm.d / 32)));
-  launch.blockDim = dim3(256);
-  launch.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  launch.attrs = attr;
-  launch.numAttrs = ctas ? 1 : 0;  // directly behind the sums' launch
-  return cuda_ok(cudaLaunchKernelEx(&launch, block_norm_bwd_finish, f)) ? MOE_OK : MOE_ERR_CUDA;
+  return launch_behind(block_norm_bwd_finish, (2 + seqs) * (dm.d / 32), 256, 0, st, f);
 }
 
 }  // namespace moe

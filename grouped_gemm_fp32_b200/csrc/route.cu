@@ -744,6 +744,7 @@ template <typename LT, int EPL, bool SOFT, bool VEC, bool GROUPS>
 __global__ void __launch_bounds__(RT_WARPS * 32, EPL == 8 ? 8 : 10)
     route_topk_kernel(const RouteArgs a) {
   __shared__ __align__(16) RouteShared sh[RT_WARPS];
+  behind();
   const int warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp;
   if (t >= a.T) return;
@@ -938,6 +939,7 @@ template <typename LT, int EPL, bool SOFT, bool VEC, bool SEQ>
 __global__ void __launch_bounds__(RT_WARPS * 32, EPL == 8 ? 8 : 10)
     route_bwd_kernel(const RouteBwdArgs a) {
   __shared__ __align__(16) double sh[RT_WARPS][RT_EMAX];
+  behind();
   const int warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp;
   if (t >= a.T) return;
@@ -961,36 +963,39 @@ void settle(bool v, F f) {
   else f(std::false_type{});
 }
 template <typename LT, int EPL>
-void start(const RouteArgs& a, cudaStream_t st) {
-  const unsigned blocks = (unsigned)((a.T + RT_WARPS - 1) / RT_WARPS);
+int start(const RouteArgs& a, cudaStream_t st) {
+  const int64_t blocks = (a.T + RT_WARPS - 1) / RT_WARPS;
+  int rc = MOE_OK;
   settle(a.softmax, [&](auto soft) {
     settle(a.vec, [&](auto vec) {
       settle(a.n_group > 1, [&](auto groups) {
-        route_topk_kernel<LT, EPL, soft.value, vec.value, groups.value>
-            <<<blocks, RT_WARPS * 32, 0, st>>>(a);
+        rc = launch_behind(route_topk_kernel<LT, EPL, soft.value, vec.value, groups.value>, blocks,
+                           RT_WARPS * 32, 0, st, a);
       });
     });
   });
+  return rc;
 }
 template <typename LT, int EPL>
-void start(const RouteBwdArgs& a, cudaStream_t st) {
-  const unsigned blocks = (unsigned)((a.T + RT_WARPS - 1) / RT_WARPS);
+int start(const RouteBwdArgs& a, cudaStream_t st) {
+  const int64_t blocks = (a.T + RT_WARPS - 1) / RT_WARPS;
+  int rc = MOE_OK;
   settle(a.softmax, [&](auto soft) {
     settle(a.vec, [&](auto vec) {
       settle(a.seq_grad != nullptr, [&](auto seq) {
-        route_bwd_kernel<LT, EPL, soft.value, vec.value, seq.value>
-            <<<blocks, RT_WARPS * 32, 0, st>>>(a);
+        rc = launch_behind(route_bwd_kernel<LT, EPL, soft.value, vec.value, seq.value>, blocks,
+                           RT_WARPS * 32, 0, st, a);
       });
     });
   });
+  return rc;
 }
 
 template <typename LT, typename Args>
 int start_for(const Args& a, cudaStream_t st) {
-  if (a.E <= 64) start<LT, 2>(a, st);
-  else if (a.E <= 128) start<LT, 4>(a, st);
-  else start<LT, 8>(a, st);
-  return cuda_ok(cudaGetLastError()) ? MOE_OK : MOE_ERR_CUDA;
+  if (a.E <= 64) return start<LT, 2>(a, st);
+  if (a.E <= 128) return start<LT, 4>(a, st);
+  return start<LT, 8>(a, st);
 }
 
 }  // namespace
