@@ -45,6 +45,7 @@ struct RouteArgs {
   int64_t T;
   int E, k, n_group, topk_group, group_top, renorm, softmax;
   int vec;  // rows of logits and probs can be read and written EPL experts at a time
+  int few;  // a token takes a few lanes, not a warp
   float scale;
 };
 
@@ -176,6 +177,12 @@ union RouteShared {
     uint2 pick[32];         // key and lane of a pick
   } f32;
   struct {
+    // of all the warp's tokens, by slot
+    uint32_t key[2 * RT_EMAX];
+    float p[2 * RT_EMAX];
+    uint2 pick[32];
+  } few;
+  struct {
     union {
       double s64[RT_EMAX];  // scores by expert, then group scores
       struct {
@@ -302,12 +309,14 @@ __device__ __forceinline__ float quick_rcp(float v) {
   return r;
 }
 
+// Affinities and scores are computed by operations that are never contracted: equal logits
+// and biases give equal bits wherever they stand, so that their order is that of the experts.
 template <bool SOFT>
 __device__ __forceinline__ float affinity(float x, float m) {
-  return SOFT ? expf(x - m) : quick_rcp(1.0f + expf(-x));
+  return SOFT ? expf(x - m) : quick_rcp(__fadd_rn(1.0f, expf(-x)));
 }
 
-// A lane's best values, descending: all of them, or four of eight.
+// A lane's best values, descending: all of them, or the best four.
 template <int EPL>
 struct Best {
   static constexpr int N = EPL < 4 ? EPL : 4;
@@ -333,10 +342,12 @@ struct Best {
       order(a[0], a[1]);
     } else {
       sort4(a);
-      if constexpr (EPL == 8) {  // the larger half of two descending fours, then in order
-        sort4(a + 4);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) a[q] = max(a[q], a[7 - q]);
+      for (int n = 4; n < EPL; n += 4) {
+        // the larger half of two descending fours, then in order
+        sort4(a + n);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) a[q] = max(a[q], a[n + 3 - q]);
         order(a[0], a[2]);
         order(a[1], a[3]);
         order(a[0], a[1]);
@@ -345,6 +356,16 @@ struct Best {
     }
 #pragma unroll
     for (int q = 0; q < N; ++q) v[q] = a[q];
+  }
+  // The best of u once all of v are taken: `last` was the lowest of them.
+  __device__ __forceinline__ void refill(uint32_t (&u)[EPL], uint32_t last) {
+    int same = N;  // of v, equal to the last
+#pragma unroll
+    for (int q = 0; q < EPL; ++q) same -= u[q] > last;
+#pragma unroll
+    for (int q = 0; q < EPL; ++q)
+      if (u[q] > last || (u[q] == last && same-- > 0)) u[q] = 0;
+    of(u);
   }
   __device__ __forceinline__ void pop() {
 #pragma unroll
@@ -538,16 +559,33 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, const LT* row, f
   __syncwarp();
 }
 
-// The picks' order in 64 bits where FP32 does not settle it: of the experts whose keys are
-// `least` or more, the first picks of the token, one a lane (ascending).  `e`: lane j's pick.
-// False where there are more than 32.
-template <typename LT, int EPL>
-__device__ __noinline__ bool refine(const RouteArgs& a, const LT* row, float m, uint32_t least,
-                                    RouteShared& sh, int& e) {
-  const int lane = threadIdx.x & 31, e0 = lane * EPL;
-  int mine = 0;
+// 1 / sum of a softmax's terms, in 64 bits.
+template <typename LT>
+__device__ __noinline__ double rz_f64(const LT* row, int E, float m) {
+  double z = 0.0;
 #pragma unroll 1
-  for (int q = 0; q < EPL; ++q) mine += sh.f32.key[slot<EPL>(lane, q)] >= least;
+  for (int e = threadIdx.x & 31; e < E; e += 32) z += exp((double)load1(row + e) - (double)m);
+  return 1.0 / warp_sum(z);
+}
+
+// The picks of a token where FP32 does not settle their order, after route_token and its
+// outputs: among the experts whose keys are `least` or more, one a lane, by 64-bit scores.
+// The token's SEG lanes from `base` on hold EPL experts each, by slot in keys and ps;
+// list [64] is free.  At first 1 / z is still FP32's rz, off by 25 u of itself, which moves
+// the difference of two scores by 25 u times that of their affinities; where that is too
+// much, z is summed in 64 bits too.  False where the token needs 64 bits as a whole.
+template <typename LT, int SEG, int EPL>
+__device__ __noinline__ bool refine(const RouteArgs& a, int64_t t, float m, float rz,
+                                    uint32_t least, const uint32_t* keys, const float* ps,
+                                    int base, int* list) {
+  const int lane = threadIdx.x & 31, l = lane - base;
+  const LT* row = reinterpret_cast<const LT*>(a.logits) + t * a.E;
+  const bool has = l >= 0 && l < SEG;
+  uint32_t u[EPL], bits = 0;
+  get(keys, lane, u);
+#pragma unroll
+  for (int q = 0; q < EPL; ++q) bits |= (has && u[q] >= least ? 1u : 0u) << q;
+  const int mine = __popc(bits);
   int at = mine;  // those up to this lane's
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -557,38 +595,49 @@ __device__ __noinline__ bool refine(const RouteArgs& a, const LT* row, float m, 
   const int n = __shfl_sync(FULL, at, 31);
   if (n > 32) return false;
   at -= mine;
-  uint32_t bits = 0;
-#pragma unroll 1
-  for (int q = 0; q < EPL; ++q) bits |= (sh.f32.key[slot<EPL>(lane, q)] >= least ? 1u : 0u) << q;
   __syncwarp();
-  for (; bits; bits &= bits - 1) sh.f32.key[at++] = e0 + __ffs(bits) - 1;
+  for (; bits; bits &= bits - 1) list[at++] = l * EPL + __ffs(bits) - 1;
   __syncwarp();
-  const int c = lane < n ? (int)sh.f32.key[lane] : 0;
-  double x = load1(row + c), rz = 1.0;
-  if (a.softmax) {
-    double z = 0.0;
-#pragma unroll 1
-    for (int q = 0; q < EPL; ++q)
-      if (e0 + q < a.E) z += exp((double)load1(row + e0 + q) - (double)m);
-    rz = 1.0 / warp_sum(z);
-    x = exp(x - (double)m) * rz;
-  } else {
-    x = 1.0 / (1.0 + exp(-x));
+  const int c = list[lane < n ? lane : 0];
+  const float b = a.bias[c];
+  const double x = load1(row + c), v = exp(a.softmax ? x - (double)m : -x);
+  double unit = rz, off = a.softmax ? 0x1p-18 : 0.0;  // 64 u
+  int rank;
+  for (;;) {
+    const double p = a.softmax ? v * unit : 1.0 / (1.0 + v);
+    bool sure = true;
+    rank = 0;
+    for (int h = 0; h < n; ++h) {
+      const double dp = __shfl_sync(FULL, p, h) - p;
+      const double ds = dp + ((double)__shfl_sync(FULL, b, h) - (double)b);
+      rank += ds > 0.0 || (ds == 0.0 && h < lane);
+      sure &= fabs(ds) >= off * fabs(dp);
+    }
+    if (off == 0.0 || __all_sync(FULL, sure || lane >= n)) break;
+    unit = rz_f64(row, a.E, m);
+    off = 0.0;
   }
-  x += (double)a.bias[c];
-  int rank = 0;
-  for (int h = 0; h < n; ++h) {
-    const double v = __shfl_sync(FULL, x, h);
-    rank += v > x || (v == x && h < lane);
+  // pick `rank` and its weight; picks from n on are those that rank at -inf, already there
+  const bool pick = lane < n && rank < a.k;
+  const float p = pick ? ps[slot<EPL>(base + c / EPL, c % EPL)] : 0.0f;
+  const float sum = warp_sum(p);
+  if (!(sum > RT_SMALL_SUM) || __any_sync(FULL, pick && p < RT_TINY)) return false;
+  if (pick) {
+    const float f = a.renorm ? a.scale * quick_rcp(sum) : a.scale * (a.softmax ? rz : 1.0f);
+    a.idx[t * a.k + rank] = c;
+    a.w[t * a.k + rank] = p * f;
   }
-  __syncwarp();
-  if (lane < n) sh.f32.key[rank] = c;
-  __syncwarp();
-  if (lane < n && lane < a.k) e = (int)sh.f32.key[lane];
   return true;
 }
 
-// A token in 32 bits; false where that does not settle the choice or the weights.
+enum { RT_DONE, RT_NEAR, RT_STOP };
+
+// A token in 32 bits: RT_STOP where that does not give the weights, RT_NEAR where it may not
+// give the picks' order, which is then refine's work with what `near` holds.
+struct Near {
+  float m, rz;     // the largest logit (0 for sigmoids), 1 / z
+  uint32_t least;  // lowest key in question
+};
 //
 // Errors, with u = 2^-24: expf and the quick reciprocal are off by 2 u of their values.
 //   sigmoid  p = 1 / (1 + e): u (2 (1 - p) + 1 + 2) p <= 3 u
@@ -599,7 +648,8 @@ __device__ __noinline__ bool refine(const RouteArgs& a, const LT* row, float m, 
 // Twice that is 6 u and 50 u / z; the margins take 8 u and 64 u / z.  Adding the bias rounds
 // by u |score|; 2 u a score stand in the margin.
 template <typename LT, int EPL, bool SOFT, bool VEC, bool GROUPS>
-__device__ __forceinline__ bool route_token(const RouteArgs& a, int64_t t, RouteShared& sh) {
+__device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, RouteShared& sh,
+                                           Near& question) {
   const int lane = threadIdx.x & 31, e0 = lane * EPL;
   const LT* row = reinterpret_cast<const LT*>(a.logits) + t * a.E;
   const bool bias = a.bias != nullptr;
@@ -622,11 +672,11 @@ __device__ __forceinline__ bool route_token(const RouteArgs& a, int64_t t, Route
     z += p[q];
   }
   z = warp_sum(z);
-  if (!(z > RT_SMALL_ALL)) return false;  // nearly nothing, nothing, or a NaN
+  if (!(z > RT_SMALL_ALL)) return RT_STOP;  // nearly nothing, nothing, or a NaN
   const float rz = quick_rcp(z);
   float s[EPL];
 #pragma unroll
-  for (int q = 0; q < EPL; ++q) s[q] = p[q] * rz;
+  for (int q = 0; q < EPL; ++q) s[q] = __fmul_rn(p[q], rz);
   if (a.probs) store_row(a.probs + t * a.E, s, e0, a.E, VEC);
   const float two_dp = SOFT ? 0x1p-18f * rz : 0x1p-21f;
   // scores; without a bias the logits rank the experts, exactly
@@ -634,7 +684,7 @@ __device__ __forceinline__ bool route_token(const RouteArgs& a, int64_t t, Route
 #pragma unroll
     for (int q = 0; q < EPL; ++q) {
       if (!SOFT) s[q] = p[q];
-      if (bias) s[q] = fmaxf(s[q] + b[q], -INFINITY);  // a NaN ranks as -inf
+      if (bias) s[q] = fmaxf(__fadd_rn(s[q], b[q]), -INFINITY);  // a NaN ranks as -inf
       if (x[q] == -INFINITY) s[q] = -INFINITY;
     }
     if constexpr (GROUPS) keep_groups(a, row, m, sh, s, two_dp);
@@ -666,18 +716,9 @@ __device__ __forceinline__ bool route_token(const RouteArgs& a, int64_t t, Route
       ++gone;
     }
     if constexpr (Best<EPL>::N < EPL) {
-      if (__any_sync(FULL, gone == Best<EPL>::N)) {
-        // a lane is out of its best: the ones below the last
-        if (gone == Best<EPL>::N) {
-          int same = Best<EPL>::N;  // picks equal to the last
-#pragma unroll
-          for (int q = 0; q < EPL; ++q) same -= u[q] > last;
-#pragma unroll
-          for (int q = 0; q < EPL; ++q)
-            if (u[q] > last || (u[q] == last && same-- > 0)) u[q] = 0;
-          best.of(u);
-          gone = 0;
-        }
+      if (__any_sync(FULL, gone == Best<EPL>::N) && gone == Best<EPL>::N) {
+        best.refill(u, last);
+        gone = 0;
       }
     }
   }
@@ -698,15 +739,16 @@ __device__ __forceinline__ bool route_token(const RouteArgs& a, int64_t t, Route
     int n = __popc(__match_any_sync(FULL, id) & lower);
     for (; n > 0; --n) where &= where - 1;
   }
-  int e = mine ? src * EPL + __ffs(where) - 1 : 0;
+  const int e = mine ? src * EPL + __ffs(where) - 1 : 0;
+  bool near = false;
   if (bias) {
     const uint32_t down = __shfl_down_sync(FULL, key, 1);
     const float sc = unordered(key), dn = unordered(down);
-    bool near = lane + 1 < a.k && down != ORD_NEG_INF &&
+    near = lane + 1 < a.k && down != ORD_NEG_INF &&
                 !(sc - dn > two_dp + 0x1p-23f * (fabsf(sc) + fabsf(dn)));
     if (__any_sync(FULL, near)) {  // equal in 64 bits too?
       const int en = __shfl_down_sync(FULL, e, 1);
-      near = near && !(load1(row + e) == load1(row + en) && a.bias[e] == a.bias[en]);
+      near = near && !(load1(row + e) == load1(row + en) && a.bias[e] == a.bias[en] && e < en);
     }
     // and the first that is not picked
     const uint32_t after = __reduce_max_sync(FULL, best.v[0]);
@@ -721,21 +763,37 @@ __device__ __forceinline__ bool route_token(const RouteArgs& a, int64_t t, Route
         if (u[q] >= least && u[q] <= last)
           near |= !(u[q] == last && load1(row + e0 + q) == xl && a.bias[e0 + q] == bl);
     }
-    if (__any_sync(FULL, near) && !refine<LT, EPL>(a, row, m, least, sh, e)) return false;
+    question = {m, rz, least};
   }
-  // not: nothing was left to choose from (the last picks only, whatever order the others have)
-  const bool some = mine && key != ORD_NEG_INF;
+  const bool some = mine && key != ORD_NEG_INF;  // not: nothing was left to choose from
   const float pe = some ? sh.f32.p[slot<EPL>(e / EPL, e % EPL)] : 0.0f;
   const float sum = warp_sum(pe);
   bool bad = some && !(sum > RT_SMALL_SUM);
   if (some && pe < RT_TINY) bad |= load1(row + e) - m > -140.0f;
-  if (__any_sync(FULL, bad)) return false;
+  if (__any_sync(FULL, bad)) return RT_STOP;
   if (mine) {
-    const float f = a.renorm ? (sum == 0.0f ? 0.0f : a.scale * quick_rcp(sum)) : a.scale * (SOFT ? rz : 1.0f);
+    const float f = a.renorm ? (sum == 0.0f ? 0.0f : a.scale * quick_rcp(sum))
+                             : a.scale * (SOFT ? rz : 1.0f);
     a.idx[t * a.k + lane] = e;
     a.w[t * a.k + lane] = pe * f;
   }
-  return true;
+  return __any_sync(FULL, near) ? RT_NEAR : RT_DONE;
+}
+
+// route_token and what its answer asks for; sh.f32 is by slots of EPL experts a lane.
+template <typename LT, int EPL, bool SOFT, bool VEC, bool GROUPS>
+__device__ __forceinline__ void route_whole(const RouteArgs& a, int64_t t, RouteShared& sh) {
+  Near q;
+  const int rc = route_token<LT, EPL, SOFT, VEC, GROUPS>(a, t, sh, q);
+  if (rc == RT_DONE) return;
+  if (rc == RT_NEAR) {
+    __syncwarp();
+    if (refine<LT, 32, EPL>(a, t, q.m, q.rz, q.least, sh.f32.key, sh.f32.p, 0,
+                            reinterpret_cast<int*>(sh.f32.pick)))
+      return;
+  }
+  __syncwarp();
+  route_token_f64<LT>(a, t, sh);
 }
 
 // A warp a token: a loop over tokens with the next one's logits on their way took 1.5 times
@@ -749,8 +807,230 @@ __global__ void __launch_bounds__(RT_WARPS * 32, EPL == 8 ? 8 : 10)
   const int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp;
   if (t >= a.T) return;
   // lane j looks after pick j: more than 32 picks take the 64-bit way
-  if (a.k > 32 || !route_token<LT, EPL, SOFT, VEC, GROUPS>(a, t, sh[warp]))
-    route_token_f64<LT>(a, t, sh[warp]);
+  if (a.k > 32) route_token_f64<LT>(a, t, sh[warp]);
+  else route_whole<LT, EPL, SOFT, VEC, GROUPS>(a, t, sh[warp]);
+}
+
+// ---- several tokens a warp
+// Where there are tokens enough to fill the SMs, a token takes SEG lanes of EPL experts, and
+// the 32 / SEG tokens of a warp share the instructions of the picks, sums and checks (480 a
+// token with a warp each, 128 experts and 6 picks).  The steps are route_token's; a token
+// that its checks stop is done again by the whole warp.
+
+template <int SEG>
+__device__ __forceinline__ float seg_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < SEG; o <<= 1) v += __shfl_xor_sync(FULL, v, o);
+  return v;
+}
+template <int SEG>
+__device__ __forceinline__ uint32_t seg_max(uint32_t v) {
+#pragma unroll
+  for (int o = 1; o < SEG; o <<= 1) v = max(v, __shfl_xor_sync(FULL, v, o));
+  return v;
+}
+// Sum of a lane's values, in pairs: log2(N) roundings.
+template <int N>
+__device__ __forceinline__ float pair_sum(const float (&v)[N]) {
+  float t[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) t[q] = v[q];
+#pragma unroll
+  for (int n = N / 2; n > 0; n /= 2)
+#pragma unroll
+    for (int q = 0; q < n; ++q) t[q] += t[q + n];
+  return t[0];
+}
+
+template <typename LT, int EPL, bool SOFT, bool GROUPS>
+__device__ __noinline__ void route_token_again(const RouteArgs& a, int64_t t, RouteShared& sh) {
+  route_whole<LT, EPL, SOFT, true, GROUPS>(a, t, sh);
+}
+
+template <typename LT, int SEG, int EPL, bool SOFT, bool GROUPS>
+__global__ void __launch_bounds__(RT_WARPS * 32, 8)
+    route_topk_few_kernel(const RouteArgs a) {
+  constexpr int TOKENS = 32 / SEG;
+  constexpr uint32_t ALL = (1u << SEG) - 1;  // lanes of a segment
+  __shared__ __align__(16) RouteShared shared[RT_WARPS];
+  behind();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  RouteShared& sh = shared[warp];
+  const int64_t t0 = ((int64_t)blockIdx.x * RT_WARPS + warp) * TOKENS;
+  if (t0 >= a.T) return;
+  const int l = lane & (SEG - 1), base = lane - l, e0 = l * EPL;
+  const bool real = t0 + lane / SEG < a.T, here = e0 < a.E;
+  const int64_t t = real ? t0 + lane / SEG : a.T - 1;
+  const LT* row = reinterpret_cast<const LT*>(a.logits) + t * a.E;
+  const bool bias = a.bias != nullptr;
+  float x[EPL];
+  load_row(x, row, e0, a.E, true, -INFINITY);
+  float m = 0.0f;
+  if (SOFT) {
+    m = x[0];
+#pragma unroll
+    for (int q = 1; q < EPL; ++q) m = fmaxf(m, x[q]);
+#pragma unroll
+    for (int o = 1; o < SEG; o <<= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+    if (m == -INFINITY) m = 0.0f;
+  }
+  float p[EPL];
+#pragma unroll
+  for (int q = 0; q < EPL; ++q) p[q] = affinity<SOFT>(x[q], m);
+  const float z = seg_sum<SEG>(pair_sum(p));
+  bool bad = !(z > RT_SMALL_ALL);
+  const float rz = quick_rcp(z);
+  put(sh.few.p, lane, p);
+  float s[EPL];
+#pragma unroll
+  for (int q = 0; q < EPL; ++q) s[q] = __fmul_rn(p[q], rz);
+  if (a.probs && real) store_row(a.probs + t * a.E, s, e0, a.E, true);
+  const float two_dp = SOFT ? 0x1p-18f * rz : 0x1p-21f;
+  if (bias || GROUPS) {
+    float b[EPL];
+    if (bias) load_row(b, a.bias, e0, a.E, true, 0.0f);
+#pragma unroll
+    for (int q = 0; q < EPL; ++q) {
+      if (!SOFT) s[q] = p[q];
+      if (bias) s[q] = fmaxf(__fadd_rn(s[q], b[q]), -INFINITY);
+      if (x[q] == -INFINITY) s[q] = -INFINITY;
+    }
+  }
+  bool out = false;  // the lane's group does not stay
+  if (GROUPS) {      // a group is 1, 2, 4, ... lanes
+    const int lanes = a.E / a.n_group / EPL;
+    float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < EPL; ++q) {
+      b2 = fmaxf(b2, fminf(b1, s[q]));
+      b1 = fmaxf(b1, s[q]);
+    }
+    for (int o = 1; o < lanes; o <<= 1) {
+      const float o1 = __shfl_xor_sync(FULL, b1, o), o2 = __shfl_xor_sync(FULL, b2, o);
+      b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+      b1 = fmaxf(b1, o1);
+    }
+    const float mag = a.group_top == 2 ? fabsf(b1) + fabsf(b2) : fabsf(b1);
+    const float err = two_dp + (mag < INFINITY ? 0x1p-22f * mag : 0.0f);
+    const float mine = a.group_top == 2 ? b1 + b2 : b1;
+    const int at = l & -lanes;
+    int before = 0;
+    for (int h = 0; h < a.n_group; h += lanes) {
+      const int o = (h + l - at) * lanes;
+      const float v = __shfl_sync(FULL, mine, base + (o & (SEG - 1)));
+      before += (v > mine || (v == mine && o < at)) && h + l - at < a.n_group;
+    }
+    for (int o = 1; o < lanes; o <<= 1) before += __shfl_xor_sync(FULL, before, o);
+    out = before >= a.topk_group;
+    // ~low: the lowest score kept, as a maximum
+    uint32_t low = here && !out ? ~ordered(mine - err) : 0;
+    uint32_t high = here && out ? ordered(mine + err) : 0;
+    low = ~seg_max<SEG>(low);
+    high = seg_max<SEG>(high);
+    bad |= (here && mine != mine) || !(unordered(low) > unordered(high) || high <= ORD_NEG_INF);
+  }
+  uint32_t u[EPL];
+#pragma unroll
+  for (int q = 0; q < EPL; ++q) {
+    if (!bias) s[q] = x[q];
+    if (GROUPS && out) s[q] = -INFINITY;
+    u[q] = here ? ordered(s[q]) : 0;
+  }
+  put(sh.few.key, lane, u);
+  Best<EPL> best;
+  best.of(u);
+  uint32_t last = 0, gone = 0;
+  const uint32_t lower = ((1u << lane) - 1) & ALL << base;  // the segment's lanes before this
+  for (int j = 0; j < a.k; ++j) {
+    last = seg_max<SEG>(best.v[0]);
+    const bool has = best.v[0] == last;
+    const uint32_t those = __ballot_sync(FULL, has);
+    if (has && (those & lower) == 0) {
+      sh.few.pick[base + j] = make_uint2(last, lane);
+      best.pop();
+      ++gone;
+    }
+    if constexpr (Best<EPL>::N < EPL) {
+      if (__any_sync(FULL, gone == Best<EPL>::N) && gone == Best<EPL>::N) {
+        best.refill(u, last);
+        gone = 0;
+      }
+    }
+  }
+  __syncwarp();
+  // lane j of the segment looks after pick j
+  const bool mine = l < a.k;
+  const uint2 pick = mine ? sh.few.pick[lane] : make_uint2(0, lane);
+  const uint32_t key = pick.x;
+  const int src = (int)pick.y;
+  const uint32_t up_key = __shfl_up_sync(FULL, key, 1);
+  const int up_src = __shfl_up_sync(FULL, src, 1);
+  uint32_t where = 0;
+  get(sh.few.key, src, u);
+#pragma unroll
+  for (int q = 0; q < EPL; ++q) where |= (u[q] == key ? 1u : 0u) << q;
+  if (__any_sync(FULL, mine && l > 0 && key == up_key && src == up_src)) {
+    const unsigned long long id = mine ? (unsigned long long)key << 6 | src : 32 + lane;
+    int n = __popc(__match_any_sync(FULL, id) & ((1u << lane) - 1));
+    for (; n > 0; --n) where &= where - 1;
+  }
+  const int e = mine ? (src - base) * EPL + __ffs(where) - 1 : 0;
+  bool near = false;
+  uint32_t least = 0;
+  if (bias) {
+    const uint32_t down = __shfl_down_sync(FULL, key, 1);
+    const float sc = unordered(key), dn = unordered(down);
+    near = l + 1 < a.k && down != ORD_NEG_INF &&
+                !(sc - dn > two_dp + 0x1p-23f * (fabsf(sc) + fabsf(dn)));
+    if (__any_sync(FULL, near)) {  // equal in 64 bits too?
+      const int en = __shfl_down_sync(FULL, e, 1);
+      near = near && !(load1(row + e) == load1(row + en) && a.bias[e] == a.bias[en] && e < en);
+    }
+    const uint32_t after = seg_max<SEG>(best.v[0]);
+    const float sl = unordered(last), margin = two_dp + 0x1p-22f * fabsf(sl);
+    least = last == ORD_NEG_INF ? last + 1 : ordered(sl - margin);
+    const bool close = after > ORD_NEG_INF && after >= least;
+    if (__any_sync(FULL, close)) {  // equal in 64 bits too?
+      const int el = __shfl_sync(FULL, e, base + a.k - 1);
+      if (close) {
+        const float xl = load1(row + el), bl = a.bias[el];
+        get(sh.few.key, lane, u);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (u[i] >= least && u[i] <= last)
+            near |= !(u[i] == last && load1(row + e0 + i) == xl && a.bias[e0 + i] == bl);
+      }
+    }
+  }
+  const bool some = mine && key != ORD_NEG_INF;
+  const float pe = some ? sh.few.p[slot<EPL>(base + e / EPL, e % EPL)] : 0.0f;
+  const float sum = seg_sum<SEG>(pe);
+  bad |= some && !(sum > RT_SMALL_SUM);
+  if (some && pe < RT_TINY) bad |= load1(row + e) - m > -140.0f;
+  const uint32_t stopped = __ballot_sync(FULL, bad && real);
+  if (mine && real && !(stopped & ALL << base)) {
+    const float f = a.renorm ? (sum == 0.0f ? 0.0f : a.scale * quick_rcp(sum))
+                             : a.scale * (SOFT ? rz : 1.0f);
+    a.idx[t * a.k + l] = e;
+    a.w[t * a.k + l] = pe * f;
+  }
+  const uint32_t nears = __ballot_sync(FULL, near && real);
+  if ((stopped | nears) == 0) return;
+  uint32_t again = stopped;
+  for (int i = 0; i < TOKENS; ++i)
+    if (nears >> (i * SEG) & ~stopped >> (i * SEG) & ALL) {
+      const int from = i * SEG;
+      __syncwarp();
+      if (!refine<LT, SEG, EPL>(a, t0 + i, __shfl_sync(FULL, m, from), __shfl_sync(FULL, rz, from),
+                                __shfl_sync(FULL, least, from), sh.few.key, sh.few.p, from,
+                                reinterpret_cast<int*>(sh.few.pick)))
+        again |= 1u << from;
+    }
+  for (int i = 0; i < TOKENS; ++i)
+    if (again >> (i * SEG) & ALL) {
+      __syncwarp();  // sh and probs are free
+      route_token_again<LT, SEG * EPL / 32, SOFT, GROUPS>(a, t0 + i, sh);
+    }
 }
 
 struct RouteBwdArgs {
@@ -760,7 +1040,7 @@ struct RouteBwdArgs {
   void* dlogits;
   int64_t T, seq_len;
   int E, k, renorm, softmax;
-  int vec;  // as in RouteArgs, of logits, seq_grad and dlogits
+  int vec, few;  // as in RouteArgs, of logits, seq_grad and dlogits
   float scale;
 };
 
@@ -840,26 +1120,41 @@ __device__ __noinline__ void route_bwd_f64(const RouteBwdArgs& a, int64_t t, dou
   }
 }
 
-// A token with at most 32 picks, lane j looking after pick j; false where its affinities
-// leave FP32's range.  sh: [2][RT_EMAX], by slot.  What bounds it is latency, so the sums
-// run side by side: a softmax's sum of p dp over the picks comes from that of p dw.
-template <typename LT, int EPL, bool SOFT, bool VEC, bool SEQ>
-__device__ __forceinline__ bool route_bwd_token(const RouteBwdArgs& a, int64_t t, float* sh) {
-  const int lane = threadIdx.x & 31, e0 = lane * EPL;
+// A token takes SEG lanes of EPL experts, as in the forward, and has at most SEG picks, lane
+// j of them looking after pick j.  What bounds it is latency, so the sums run side by side:
+// a softmax's sum of p dp over the picks comes from that of p dw.  Tokens whose affinities
+// leave FP32's range, or with more picks, are done in 64 bits.
+template <typename LT, int SEG, int EPL, bool SOFT, bool VEC, bool SEQ>
+__global__ void __launch_bounds__(RT_WARPS * 32, EPL == 8 ? 8 : 10)
+    route_bwd_kernel(const RouteBwdArgs a) {
+  constexpr int TOKENS = 32 / SEG;
+  constexpr uint32_t ALL = SEG == 32 ? FULL : (1u << SEG % 32) - 1;
+  __shared__ __align__(16) double sh[RT_WARPS][RT_EMAX];
+  behind();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t0 = ((int64_t)blockIdx.x * RT_WARPS + warp) * TOKENS;
+  if (t0 >= a.T) return;
+  if (a.k > SEG) {  // of SEG = 32 only
+    route_bwd_f64<LT>(a, t0, sh[warp]);
+    return;
+  }
+  const int l = lane & (SEG - 1), base = lane - l, e0 = l * EPL;
+  const bool real = t0 + lane / SEG < a.T;
+  const int64_t t = real ? t0 + lane / SEG : a.T - 1;
+  float* dp = reinterpret_cast<float*>(sh[warp]);  // the picks' dp, by slot
   const LT* row = reinterpret_cast<const LT*>(a.logits) + t * a.E;
-  const bool mine = lane < a.k;
-  const int e = mine ? a.idx[t * a.k + lane] : -1;
-  const float wj = mine ? a.w[t * a.k + lane] : 0.0f, dwj = mine ? a.dw[t * a.k + lane] : 0.0f;
+  const bool mine = l < a.k;
+  const int e = mine ? a.idx[t * a.k + l] : -1;
+  const float wj = mine ? a.w[t * a.k + l] : 0.0f, dwj = mine ? a.dw[t * a.k + l] : 0.0f;
   const bool ok = wj != 0.0f && e >= 0 && e < a.E;
-  const int se = ok ? slot<EPL>(e / EPL, e % EPL) : 0;
-  float* ps = sh;            // affinities
-  float* dp = sh + RT_EMAX;  // the picks' dp
+  const int se = ok ? slot<EPL>(base + e / EPL, e % EPL) : 0;
   float x[EPL], sg[EPL];
   load_row(x, row, e0, a.E, VEC, -INFINITY);
   if (SEQ) {
     const uint32_t len = (uint32_t)min(a.seq_len, (int64_t)0x7fffffff);  // T is below 2^31
     load_row(sg, a.seq_grad + (int64_t)((uint32_t)t / len) * a.E, e0, a.E, VEC, 0.0f);
   }
+  const float xe = ok ? load1(row + e) : 0.0f;
   // does an expert stand twice among the picks?
   if (ok) dp[se] = __int_as_float(lane);
   __syncwarp();
@@ -875,7 +1170,12 @@ __device__ __forceinline__ bool route_bwd_token(const RouteBwdArgs& a, int64_t t
     m = x[0];
 #pragma unroll
     for (int q = 1; q < EPL; ++q) m = fmaxf(m, x[q]);
-    m = warp_max(m);
+    if (SEG == 32) {
+      m = warp_max(m);
+    } else {
+#pragma unroll
+      for (int o = 1; o < SEG; o <<= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+    }
     if (m == -INFINITY) m = 0.0f;
   }
 #pragma unroll
@@ -888,9 +1188,7 @@ __device__ __forceinline__ bool route_bwd_token(const RouteBwdArgs& a, int64_t t
       s1[q] = h * r * r;
     }
   }
-  put(ps, lane, p);
-  __syncwarp();
-  const float pe = ok ? ps[se] : 0.0f;
+  const float pe = ok ? affinity<SOFT>(xe, m) : 0.0f;
   // all sums in one round: over the picks p, dw w and p dw, over the experts p and p g
   float sum[5] = {pe, ok ? dwj * wj : 0.0f, ok ? pe * dwj : 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -899,29 +1197,30 @@ __device__ __forceinline__ bool route_bwd_token(const RouteBwdArgs& a, int64_t t
     if (SEQ) sum[4] = fmaf(p[q], sg[q], sum[4]);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int o = SEG / 2; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < 5; ++i) sum[i] += __shfl_xor_sync(FULL, sum[i], o);
   const float z = sum[3], rz = z == 0.0f ? 0.0f : quick_rcp(z);
-  if (!SOFT && SEQ && z < RT_SMALL_ALL) return false;
-  const bool any = __any_sync(FULL, ok);
+  bool bad = !SOFT && SEQ && z < RT_SMALL_ALL;
+  const bool any = (__ballot_sync(FULL, ok) & ALL << base) != 0;
   const float unit = SOFT ? rz : 1.0f;  // of p
   float d = a.scale * dwj, cp = a.scale * sum[2] * unit;  // cp: sum of p dp over the picks
   if (a.renorm) {
-    if (any && sum[0] < RT_SMALL_SUM) return false;
+    bad |= any && sum[0] < RT_SMALL_SUM;
     const float r = any ? 1.0f / sum[0] : 0.0f;  // 1 / sum of the picks' p z
     d = (d - sum[1]) * r * (SOFT ? z : 1.0f);
     cp = a.scale * sum[2] * r - (any ? sum[1] : 0.0f);
   }
   if (twice) {  // both terms, in the picks' order
-    const unsigned same = __match_any_sync(FULL, ok ? e : -1 - lane);
+    const unsigned same = __match_any_sync(FULL, ok ? base << 16 | e : -1 - lane);
     float v = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
+    for (int j = 0; j < 32; ++j) {
       const float o = __shfl_sync(FULL, d, j);
       if (same >> j & 1) v += o;
     }
     d = v;
   }
+  __syncwarp();
   if (ok) dp[se] = d;
   __syncwarp();
   get(dp, lane, g);
@@ -931,27 +1230,29 @@ __device__ __forceinline__ bool route_bwd_token(const RouteBwdArgs& a, int64_t t
     if (SOFT) g[q] = p[q] * rz * (SEQ ? g[q] + sg[q] - (cp + cg) : g[q] - cp);
     else g[q] = s1[q] * (SEQ ? g[q] + (sg[q] - cg) * rz : g[q]);
   }
-  store_row(reinterpret_cast<LT*>(a.dlogits) + t * a.E, g, e0, a.E, VEC);
-  return true;
+  if (real) store_row(reinterpret_cast<LT*>(a.dlogits) + t * a.E, g, e0, a.E, VEC);
+  const uint32_t stopped = __ballot_sync(FULL, bad && real);
+  if (stopped)
+    for (int i = 0; i < TOKENS; ++i)
+      if (stopped >> (i * SEG) & ALL) {
+        __syncwarp();  // sh and the row are free
+        route_bwd_f64<LT>(a, t0 + i, sh[warp]);
+      }
 }
 
-template <typename LT, int EPL, bool SOFT, bool VEC, bool SEQ>
-__global__ void __launch_bounds__(RT_WARPS * 32, EPL == 8 ? 8 : 10)
-    route_bwd_kernel(const RouteBwdArgs a) {
-  __shared__ __align__(16) double sh[RT_WARPS][RT_EMAX];
-  behind();
-  const int warp = threadIdx.x >> 5;
-  const int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp;
-  if (t >= a.T) return;
-  float* f32 = reinterpret_cast<float*>(sh[warp]);
-  if (a.k > 32 || !route_bwd_token<LT, EPL, SOFT, VEC, SEQ>(a, t, f32))
-    route_bwd_f64<LT>(a, t, sh[warp]);
+// Whether a token takes a few lanes of eight experts each, up to 128 experts: 8 lanes of 64,
+// 16 of 128.  With 16384 tokens of 64 experts the forward took 6.8 us instead of 11.3, of
+// 128 experts 11.1 instead of 12.9; with 2048 tokens and fewer a warp each is as fast or
+// faster (128 experts: 3.2 against 3.7 us), for its shorter chain of steps.  Of 256
+// experts, 16 lanes of 16 took 18.3 us instead of 16.5.
+bool few_lanes(const moe_dims& dm) {
+  return dm.T >= 2560 && dm.E <= 128 && dm.k <= (dm.E <= 64 ? 8 : 16);
 }
 
-// Whether rows of E experts from p on can be taken EPL at a time: whole pieces that start
-// on their alignment.
-bool in_pieces(const void* p, int E, int size) {
-  const int epl = E <= 64 ? 2 : E <= 128 ? 4 : 8;
+// Whether rows of E experts from p on can be taken a lane's share at a time: whole pieces
+// that start on their alignment.
+bool in_pieces(const void* p, int E, int size, bool few = false) {
+  const int epl = few ? 8 : E <= 64 ? 2 : E <= 128 ? 4 : 8;
   const int piece = epl * size < 16 ? epl * size : 16;
   return E % epl == 0 && reinterpret_cast<uintptr_t>(p) % piece == 0;
 }
@@ -964,6 +1265,20 @@ void settle(bool v, F f) {
 }
 template <typename LT, int EPL>
 int start(const RouteArgs& a, cudaStream_t st) {
+  if constexpr (EPL < 8) {
+    constexpr int SEG = EPL * 4, PER = 8;
+    if (a.few) {
+      const int64_t tokens = RT_WARPS * 32 / SEG, blocks = (a.T + tokens - 1) / tokens;
+      int rc = MOE_OK;
+      settle(a.softmax, [&](auto soft) {
+        settle(a.n_group > 1, [&](auto groups) {
+          rc = launch_behind(route_topk_few_kernel<LT, SEG, PER, soft.value, groups.value>, blocks,
+                             RT_WARPS * 32, 0, st, a);
+        });
+      });
+      return rc;
+    }
+  }
   const int64_t blocks = (a.T + RT_WARPS - 1) / RT_WARPS;
   int rc = MOE_OK;
   settle(a.softmax, [&](auto soft) {
@@ -976,19 +1291,26 @@ int start(const RouteArgs& a, cudaStream_t st) {
   });
   return rc;
 }
-template <typename LT, int EPL>
-int start(const RouteBwdArgs& a, cudaStream_t st) {
-  const int64_t blocks = (a.T + RT_WARPS - 1) / RT_WARPS;
+template <typename LT, int SEG, int EPL, bool FEW>
+int start_bwd(const RouteBwdArgs& a, cudaStream_t st) {
+  const int64_t tokens = RT_WARPS * 32 / SEG, blocks = (a.T + tokens - 1) / tokens;
   int rc = MOE_OK;
   settle(a.softmax, [&](auto soft) {
-    settle(a.vec, [&](auto vec) {
+    settle(FEW || a.vec, [&](auto vec) {
       settle(a.seq_grad != nullptr, [&](auto seq) {
-        rc = launch_behind(route_bwd_kernel<LT, EPL, soft.value, vec.value, seq.value>, blocks,
-                           RT_WARPS * 32, 0, st, a);
+        if constexpr (vec.value || !FEW)
+          rc = launch_behind(route_bwd_kernel<LT, SEG, EPL, soft.value, vec.value, seq.value>,
+                             blocks, RT_WARPS * 32, 0, st, a);
       });
     });
   });
   return rc;
+}
+template <typename LT, int EPL>
+int start(const RouteBwdArgs& a, cudaStream_t st) {
+  if constexpr (EPL < 8)
+    if (a.few) return start_bwd<LT, EPL * 4, 8, true>(a, st);
+  return start_bwd<LT, 32, EPL, false>(a, st);
 }
 
 template <typename LT, typename Args>
@@ -1020,6 +1342,12 @@ int launch_route_topk(const moe_dims& dm, const moe_route_cfg& c, int type, cons
   a.scale = c.scale;
   a.vec = in_pieces(logits, dm.E, type == MOE_F32 ? 4 : 2) && in_pieces(probs, dm.E, 4) &&
           in_pieces(bias, dm.E, 4);
+  a.few = few_lanes(dm) && in_pieces(logits, dm.E, type == MOE_F32 ? 4 : 2, true) &&
+          in_pieces(probs, dm.E, 4, true) && in_pieces(bias, dm.E, 4, true);
+  if (a.n_group > 1) {  // groups in whole lanes
+    const int lanes = dm.E / a.n_group / 8;
+    a.few &= lanes * 8 * a.n_group == dm.E && (lanes & (lanes - 1)) == 0;
+  }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return type == MOE_F32 ? start_for<float>(a, st) : start_for<__nv_bfloat16>(a, st);
 }
@@ -1045,6 +1373,8 @@ int launch_route_bwd(const moe_dims& dm, const moe_route_cfg& c, int type, const
   const int size = type == MOE_F32 ? 4 : 2;
   a.vec = in_pieces(logits, dm.E, size) && in_pieces(dlogits, dm.E, size) &&
           in_pieces(seq_grad, dm.E, 4);
+  a.few = few_lanes(dm) && in_pieces(logits, dm.E, size, true) &&
+          in_pieces(dlogits, dm.E, size, true) && in_pieces(seq_grad, dm.E, 4, true);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return type == MOE_F32 ? start_for<float>(a, st) : start_for<__nv_bfloat16>(a, st);
 }

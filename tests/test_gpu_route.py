@@ -288,3 +288,102 @@ def test_gate_logits_and_bwd(T, d, E, k):
     rx = dx0.double() + dl.double() @ wg.double()
     ref64.within(dx, rx, 1e-2 * rx.abs().amax(), "dx")
     assert moe.moe_get_device_status(ws) == 0
+
+
+# ---- from 2560 tokens on, a token of up to 128 experts takes a few lanes of a warp
+
+MANY = 2563      # an odd number: the last warp's lanes are not all taken
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("E,k", [(8, 1), (8, 8), (16, 3), (64, 8), (64, 9), (72, 16), (120, 5),
+                                 (128, 16), (128, 17), (100, 6)])
+def test_many_tokens_match_64_bits(E, k, score):
+    for dtype, bias in itertools.product((torch.float32, torch.bfloat16), (True, False)):
+        check(*make(MANY, E, k, E + k, bias, dtype, score=score, scale=2.5))
+    x, b, cfg = make(MANY, E, k, E, True, torch.bfloat16, score=score)
+    check(x, torch.zeros_like(b), cfg)            # many equal scores
+    check(x, b.round(decimals=2), cfg)
+    check(*make(MANY, E, k, E + 1, score=score, renorm=False))
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("E,G,K,top,k", [(128, 8, 4, 2, 8), (128, 4, 1, 2, 6), (128, 16, 3, 1, 9),
+                                         (64, 2, 1, 2, 8), (64, 8, 3, 1, 3), (96, 3, 2, 2, 5)])
+def test_groups_of_many_tokens_match_64_bits(E, G, K, top, k, score):
+    for dtype, bias in itertools.product((torch.float32, torch.bfloat16), (True, False)):
+        x, b, cfg = make(MANY, E, k, E + G, bias, dtype, score=score, n_group=G, topk_group=K,
+                         group_top=top, scale=1.5)
+        check(x, b, cfg)
+        x[::3] = x[::3].round()                   # groups of equal scores too
+        check(x, b, cfg)
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("E", [64, 128])
+def test_many_tokens_near_equal_masked_and_extreme(E, score):
+    T = MANY
+    g = torch.Generator(device="cuda").manual_seed(E)
+    base = torch.randint(0, 4, (T, E), generator=g, device="cuda").float()
+    x = base + 2.0 ** -22 * torch.randint(0, 4, (T, E), generator=g, device="cuda")
+    b = 2.0 ** -26 * torch.randint(0, 8, (E,), generator=g, device="cuda").float()
+    for groups in (dict(), dict(n_group=4, topk_group=2)):
+        cfg = dict(score=score, n_group=1, topk_group=1, group_top=2, renorm=True, scale=1.0,
+                   k=6) | groups
+        check(x, b, cfg)
+        check(x, None, cfg)
+        check(base, b * 0, cfg)
+        y, c, _ = make(T, E, 6, 3)
+        y[::5] = -INF                             # tokens without any expert beside others
+        y[1::5, 3:] = -INF
+        y[2::5, ::2] = -INF
+        y[3::5, ::3] = torch.finfo(torch.float32).min
+        check(y, c, cfg)
+        c[5:E // 2] = -INF
+        check(y, c, cfg)
+        check(*make(T, E, 6, 4, std=30.0, **{n: cfg[n] for n in cfg if n != "k"}))
+    # a token with NaN or infinite logits leaves its neighbours in the warp alone
+    x, b, cfg = make(T, E, 6, 6, score=score)
+    x[0, 5], x[9], x[18, 7], x[27, 1] = math.nan, math.nan, INF, -INF
+    _, _, idx, w, p = call(x, b, cfg)
+    ridx, rw, rp, _ = ref64.route(x, b, cfg)
+    assert torch.equal(idx, ridx)
+    assert torch.equal(w.isnan(), rw.isnan()) and torch.equal(p.isnan(), rp.isnan())
+    fin = ~rw.isnan()
+    ref64.within(w[fin], rw[fin], 2 * (24 + 16) * 2.0 ** -23 * rw[fin], "weights")
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("E,k,L", [(8, 8, 0), (64, 8, 2000), (64, 5, 0), (128, 16, 700),
+                                   (128, 6, 0), (96, 7, 1), (100, 6, 130), (64, 12, 50)])
+def test_bwd_of_many_tokens(E, k, L, score):
+    for dtype, renorm in itertools.product((torch.float32, torch.bfloat16), (True, False)):
+        x, b, cfg = make(MANY, E, k, E * k, True, dtype, score=score, scale=2.5, renorm=renorm)
+        x[7] = -INF
+        x[8, 3:] = -INF
+        dm, rc, idx, w, _ = call(x, b, cfg)
+        g = torch.Generator(device="cuda").manual_seed(E)
+        dw = torch.randn(MANY, k, generator=g, device="cuda")
+        sg = torch.randn(-(-MANY // L), E, generator=g, device="cuda") if L else None
+        bwd_check(x, idx, w, dw, cfg, rc, dm, sg, L)
+        idx = idx.clone()
+        idx[3, 0], idx[4, k - 1], idx[5, 0] = -1, E, 1 << 30       # no expert: skipped
+        if k > 1:
+            idx[6, 1] = idx[6, 0]                 # the same expert twice
+            idx[MANY - 1, k - 1] = idx[MANY - 1, 0]
+        if k > 2:
+            idx[100, 2] = idx[100, 1] = idx[100, 0]
+        bwd_check(x, idx, w, dw, cfg, rc, dm, sg, L)
+
+
+def test_many_tokens_on_unaligned_views():
+    # bases off the 16-byte pieces: element-wise accesses, the same results
+    x, b, cfg = make(MANY, 64, 6, 9, dtype=torch.bfloat16)
+    flat = torch.zeros(x.numel() + 1, dtype=x.dtype, device="cuda")
+    y = flat[1:].view_as(x)
+    y.copy_(x)
+    _, _, i1, w1, p1 = call(x, b, cfg)
+    _, _, i2, w2, p2 = call(y, b, cfg)
+    assert torch.equal(i1, i2)
+    ref64.within(w2, w1, 2.0 ** -20 * w1, "weights")
+    ref64.within(p2, p1, 2.0 ** -20 * p1, "probs")
