@@ -5,10 +5,12 @@
 // writes it once.  The list travels as a kernel argument (up to GL_MAX tensors a
 // launch), so nothing is copied to the device and a captured graph holds its own.
 //
-// A launch splits its tensors into chunks of up to GL_CHUNK elements of one tensor
-// each; CTA b takes chunks b, b + gridDim, ... .  Squares are exact in 64 bits (an
-// FP32 value's square has 48 significant bits) and are added in 64 bits: no overflow,
-// no lost small elements.  Every sum runs in an order fixed by the list's sizes.
+// A launch splits its tensors into chunks of up to GL_CHUNK elements of one tensor each;
+// CTA b takes chunks b, b + gridDim, ... .  Squares are exact in 64 bits (an FP32 value's
+// square has 48 significant bits) and are added in 64 bits: no overflow, no lost small
+// elements.  Every sum runs in an order fixed by the list's sizes.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -20,9 +22,13 @@ namespace {
 
 constexpr int GL_MAX = 512;      // tensors per launch
 constexpr int GL_FEW = 48;       // of a launch with the short table
-constexpr int GL_CTAS = 592;     // CTAs of a launch (four an SM); a norm launch's partial sums
+// CTAs of a norm's launch (and its partial sums) and of a clipping's, at most: ten and 24 an
+// SM, of which four run at a time.  With four each, 60 M bf16 elements took 67 us instead of
+// 62 and 624 M FP32 ones 596 instead of 560: a CTA that is done early makes room.
+constexpr int GL_CTAS = 148 * 10;
+constexpr int GL_CLIP_CTAS = 148 * 24;
 constexpr int GL_THREADS = 256;
-constexpr int GL_CHUNK = 16384;  // most elements of a chunk: 8 vectors a thread of bf16
+constexpr int GL_CHUNK = 32768;  // most elements of a chunk: 16 vectors a thread of bf16
 constexpr int GL_CHUNK_MIN = 2048;
 
 struct GradEnt {
@@ -78,51 +84,110 @@ __device__ __forceinline__ void add_square(double& s, float v) {
   s = fma(d, d, s);
 }
 
-__device__ __forceinline__ void add_squares(double (&s)[4], const uint4& u, const float*) {
-  add_square(s[0], __uint_as_float(u.x));
-  add_square(s[1], __uint_as_float(u.y));
-  add_square(s[2], __uint_as_float(u.z));
-  add_square(s[3], __uint_as_float(u.w));
-}
-__device__ __forceinline__ void add_squares(double (&s)[4], const uint4& u,
-                                            const __nv_bfloat16*) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    add_square(s[i], __uint_as_float(w[i] << 16));
-    add_square(s[i], __uint_as_float(w[i] & 0xffff0000u));
-  }
-}
-__device__ __forceinline__ void add_squares(double (&s)[4], const uint4& u, const __half*) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    add_square(s[i], f.x);
-    add_square(s[i], f.y);
-  }
-}
-
+// The sum of a thread's squares.  FP32 elements are converted; of 16-bit ones a thread has
+// twice as many in the same time, so theirs come from the bits: those of |x| as FP32, three
+// places down and with 896 added to the exponent, are those of |x| in 64 bits where x is
+// normal.  A zero or subnormal x stands there as a number below 2^-126, whose square is
+// nothing beside that of a 2^-60.  `top` collects the largest |x|: a run with infinities or
+// NaN, or with nothing above 2^-60, is summed again by conversion, and one of zeros is 0.
 template <typename T>
-__device__ __noinline__ void chunk_sum(double (&s)[4], const void* data, int64_t i0, int64_t i1) {
-  constexpr int N = 16 / sizeof(T), UNROLL = 8;
+struct Squares {
+  static constexpr bool BITS = sizeof(T) == 2;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  uint32_t top = 0;  // two 16-bit patterns
+
+  // hi: the pattern of |x| in FP32, three places down; its last 13 bits were zero
+  __device__ __forceinline__ static void add_bits(double& to, uint32_t hi) {
+    const double d = __hiloint2double((int)(hi + (896u << 20)), 0);
+    to = fma(d, d, to);
+  }
+  __device__ __forceinline__ void add(const uint4& u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (!BITS) {
+        add_square(s[i], __uint_as_float(w[i]));
+      } else {
+        top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+        if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+          add_bits(s[i], (w[i] & 0x7fffu) << 13);
+          add_bits(s[i], w[i] >> 3 & 0x0fffe000u);
+        } else {  // as FP32 a half is normal or zero
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+          const uint32_t a = __float_as_uint(f.x) & 0x7fffffffu;
+          const uint32_t b = __float_as_uint(f.y) & 0x7fffffffu;
+          add_bits(s[i], a >> 3);
+          add_bits(s[i], b >> 3);
+        }
+      }
+    }
+  }
+  // The run has to be summed by conversion.
+  __device__ __forceinline__ bool again() const {
+    if constexpr (!BITS) return false;
+    constexpr bool BF = std::is_same_v<T, __nv_bfloat16>;
+    constexpr uint32_t INF = BF ? 0x7f80u : 0x7c00u, LOW = BF ? (127u - 60u) << 7 : 1u;
+    const uint32_t m = max(top >> 16, top & 0xffffu);
+    return m >= INF || (m != 0 && m < LOW);
+  }
+  __device__ __forceinline__ double total() const {
+    return BITS && top == 0 ? 0.0 : (s[0] + s[1]) + (s[2] + s[3]);
+  }
+};
+
+// The squares of elements [i0, i1).
+template <typename T>
+__device__ __noinline__ double run_sum(const void* data, int64_t i0, int64_t i1) {
+  constexpr int N = 16 / sizeof(T), BATCH = 4;
   const T* p = reinterpret_cast<const T*>(data);
   int64_t v0, v1;
   vector_part(p, i0, i1, v0, v1);
-  const uint4* v = reinterpret_cast<const uint4*>(p + v0);
-  const int n = (int)((v1 - v0) / N);
-  int i0v = threadIdx.x;
-  for (; i0v + (UNROLL - 1) * GL_THREADS < n; i0v += UNROLL * GL_THREADS) {
-    uint4 u[UNROLL];
+  const uint4* v = reinterpret_cast<const uint4*>(p + v0) + threadIdx.x;
+  const int64_t n = (v1 - v0) / N - threadIdx.x;  // from this thread's first on
+  Squares<T> q;
+  auto load = [&](uint4 (&u)[BATCH]) {
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) u[k] = __ldg(v + i0v + k * GL_THREADS);
+    for (int k = 0; k < BATCH; ++k) u[k] = __ldg(v + k * GL_THREADS);
+    v += BATCH * GL_THREADS;
+  };
+  auto add = [&](const uint4 (&u)[BATCH]) {
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) add_squares(s, u[k], p);
+    for (int k = 0; k < BATCH; ++k) q.add(u[k]);
+  };
+  // two batches take turns, one on its way while the other is added
+  int64_t left = n > 0 ? (n - 1) / GL_THREADS + 1 : 0;  // this thread's vectors
+  if (left >= BATCH) {
+    uint4 a[BATCH], b[BATCH];
+    load(a);
+    left -= BATCH;
+    for (; left >= 2 * BATCH; left -= 2 * BATCH) {
+      load(b);
+      add(a);
+      load(a);
+      add(b);
+    }
+    if (left >= BATCH) {
+      load(b);
+      left -= BATCH;
+      add(a);
+      add(b);
+    } else {
+      add(a);
+    }
   }
 #pragma unroll 1
-  for (; i0v < n; i0v += GL_THREADS) add_squares(s, __ldg(v + i0v), p);
-  for (int64_t i = i0 + threadIdx.x; i < v0; i += GL_THREADS) add_square(s[0], to_f32(p[i]));
-  for (int64_t i = v1 + threadIdx.x; i < i1; i += GL_THREADS) add_square(s[0], to_f32(p[i]));
+  for (; left > 0; --left, v += GL_THREADS) q.add(__ldg(v));
+  double s = q.total();
+  if (q.again()) {
+    s = 0.0;
+#pragma unroll 1
+    for (int64_t i = threadIdx.x; i < (v1 - v0) / N; i += GL_THREADS)
+#pragma unroll 1
+      for (int k = 0; k < N; ++k) add_square(s, to_f32(p[v0 + i * N + k]));
+  }
+  for (int64_t e = i0 + threadIdx.x; e < v0; e += GL_THREADS) add_square(s, to_f32(p[e]));
+  for (int64_t e = v1 + threadIdx.x; e < i1; e += GL_THREADS) add_square(s, to_f32(p[e]));
+  return s;
 }
 
 __device__ double block_sum(double v) {
@@ -140,16 +205,16 @@ template <int N>
 __global__ void __launch_bounds__(GL_THREADS, 4)
     grad_sumsq_kernel(const __grid_constant__ GradTable<N> tb, double* __restrict__ part) {
   behind();
-  double acc[4] = {0.0, 0.0, 0.0, 0.0};
+  double s = 0.0;
   for (int64_t c = blockIdx.x; c < tb.chunks; c += gridDim.x) {
     const int k = find(tb, c);
-    const int64_t i0 = (c - tb.e[k].chunk0) * tb.chunk;
-    const int64_t i1 = min(i0 + tb.chunk, tb.e[k].n);
-    if (tb.type[k] == MOE_F32) chunk_sum<float>(acc, tb.e[k].data, i0, i1);
-    else if (tb.type[k] == MOE_BF16) chunk_sum<__nv_bfloat16>(acc, tb.e[k].data, i0, i1);
-    else chunk_sum<__half>(acc, tb.e[k].data, i0, i1);
+    const GradEnt& e = tb.e[k];
+    const int64_t i0 = (c - e.chunk0) * tb.chunk, i1 = min(i0 + tb.chunk, e.n);
+    if (tb.type[k] == MOE_F32) s += run_sum<float>(e.data, i0, i1);
+    else if (tb.type[k] == MOE_BF16) s += run_sum<__nv_bfloat16>(e.data, i0, i1);
+    else s += run_sum<__half>(e.data, i0, i1);
   }
-  const double s = block_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+  s = block_sum(s);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
@@ -204,24 +269,42 @@ __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, uint32_
 
 // Vectors of out that are 16-byte aligned, out of data that may not be: `u` points at the
 // 16 bytes that hold the first one's first element, which stands 4 WS + bits / 8 bytes in.
-// WS < 0: data is aligned too.
+// WS < 0: data is aligned too.  A warp takes neighbouring vectors, some a lane at a time; the words
+// that a vector needs of the next one come from the next lane.
 template <typename T, int WS>
 __device__ __noinline__ void scale_vectors(const uint4* u, uint4* o, int n, uint32_t bits, float f) {
-  constexpr int UNROLL = WS < 0 ? 8 : 4;
-  auto load = [&](int j) {
-    if constexpr (WS < 0) return u[j];
-    else return shifted<WS>(u[j], u[j + 1], bits);  // the second from the L1: the next thread's
-  };
-  int i = threadIdx.x;
-  for (; i + (UNROLL - 1) * GL_THREADS < n; i += UNROLL * GL_THREADS) {
-    uint4 a[UNROLL];
+  constexpr int BATCH = WS < 0 ? 8 : 4;
+  const int lane = threadIdx.x & 31;
+  int i = (threadIdx.x >> 5) * 32 * BATCH;
+  for (; i + 32 * BATCH <= n; i += GL_THREADS * BATCH) {
+    uint4 a[BATCH + 1];
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) a[k] = load(i + k * GL_THREADS);
+    for (int k = 0; k < BATCH; ++k) a[k] = u[i + 32 * k + lane];
+    if constexpr (WS >= 0) a[BATCH] = lane == 0 ? u[i + 32 * BATCH] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) o[i + k * GL_THREADS] = scale(a[k], f, (const T*)nullptr);
+    for (int k = 0; k < BATCH; ++k) {
+      if constexpr (WS >= 0) {
+        // lane 31's next vector is lane 0's of the next 32
+        const uint4 g = lane == 0 ? a[k + 1] : a[k];
+        const int from = lane + 1 & 31;
+        uint4 b = make_uint4(0, 0, 0, 0);
+        b.x = __shfl_sync(0xffffffffu, g.x, from);
+        if (WS > 0) b.y = __shfl_sync(0xffffffffu, g.y, from);
+        if (WS > 1) b.z = __shfl_sync(0xffffffffu, g.z, from);
+        if (WS > 2) b.w = __shfl_sync(0xffffffffu, g.w, from);
+        o[i + 32 * k + lane] = scale(shifted<WS>(a[k], b, bits), f, (const T*)nullptr);
+      } else {
+        o[i + 32 * k + lane] = scale(a[k], f, (const T*)nullptr);
+      }
+    }
   }
-#pragma unroll 1
-  for (; i < n; i += GL_THREADS) o[i] = scale(load(i), f, (const T*)nullptr);
+  // fewer than a warp's share are left
+  i = n / (32 * BATCH) * (32 * BATCH) + threadIdx.x;
+  if (i < n) {
+    uint4 a = u[i];
+    if constexpr (WS >= 0) a = shifted<WS>(a, u[i + 1], bits);
+    o[i] = scale(a, f, (const T*)nullptr);
+  }
 }
 
 // out[i] = f data[i] for a chunk [i0, i1) of a tensor of n elements.
@@ -360,7 +443,7 @@ static int clip_with(const moe_grad* g, int64_t n, const double* part, int64_t p
   do {
     GradTable<N> tb;
     fill(tb, g, n, &i);
-    const int64_t ctas = tb.chunks < GL_CTAS ? (tb.chunks > 0 ? tb.chunks : 1) : GL_CTAS;
+    const int64_t ctas = tb.chunks < GL_CLIP_CTAS ? (tb.chunks > 0 ? tb.chunks : 1) : GL_CLIP_CTAS;
     const int rc = launch_behind(grad_clip_kernel<N>, ctas, GL_THREADS, 0, st, tb, part, parts,
                                  sumsq, max_norm, norm, coef);
     if (rc != MOE_OK) return rc;

@@ -174,3 +174,36 @@ def test_streams_graphs_and_the_same_bits():
         torch.cuda.synchronize()
         for t, r in zip(outs + [s["sumsq"], s["norm"], s["coef"]], ref):
             assert torch.equal(t, r)
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float16, torch.float32])
+def test_runs_of_zeros_tiny_and_subnormal_elements(t):
+    # long runs (whole vectors) whose squares are those of a type's smallest numbers, alone
+    # and beside ordinary ones; a run of zeros gives exactly 0
+    n = 40_000
+    info = torch.finfo(t)
+    least = {torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -24, torch.float32: 2.0 ** -149}[t]
+    for v in (0.0, least, 5 * least, info.tiny, 3 * info.tiny, 2.0 ** -60 if t != torch.float16
+              else 2.0 ** -14, 1.0):
+        x = torch.full((n,), v, dtype=t, device="cuda")
+        x[::2] *= -1
+        s = state(moe.GradList([x]))
+        moe.moe_grad_norm(moe.GradList([x]), 0, s["sumsq"], s["norm"], s["ws"])
+        want = n * float(x[0].double()) ** 2
+        # n sums of exact squares in 64 bits, each within 2^-53
+        assert abs(float(s["sumsq"]) - want) <= n * 2.0 ** -53 * want, v
+        y = torch.cat([x, torch.tensor([0.5], dtype=t, device="cuda")])
+        moe.moe_grad_norm(moe.GradList([y]), 0, s["sumsq"], s["norm"], s["ws"])
+        assert abs(float(s["sumsq"]) - want - 0.25) <= n * 2.0 ** -53 * (want + 0.25), v
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_one_non_finite_element_in_a_long_run(t, bad):
+    for at in (0, 8, 12_345, 39_999):
+        x = torch.ones(40_000, dtype=t, device="cuda")
+        x[at] = bad
+        s = state(moe.GradList([x]))
+        moe.moe_grad_norm(moe.GradList([x]), 0, s["sumsq"], s["norm"], s["ws"])
+        got = float(s["norm"])
+        assert math.isnan(got) if math.isnan(bad) else got == math.inf
