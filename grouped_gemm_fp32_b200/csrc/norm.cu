@@ -93,11 +93,45 @@ __device__ __forceinline__ F8 from_bf16(const uint4& u) {
     r.v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   return r;
 }
-__device__ __forceinline__ F8 ld8(const float* p) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+// Which eight columns of a row a thread has as vector c: [a, a + 4) and [b, b + 4).  With a
+// bf16 residual they are the 16 bytes of vector c.  With an FP32 one they lie in the two
+// halves of the columns of the warp's vectors, so that a warp's 16-byte accesses to FP32
+// rows and its 8-byte accesses to bf16 ones are each contiguous (side by side, the eight
+// would be half sectors of the L2 apart: 16384 x 7168 took 303 us forward).
+struct Cols {
+  int a, b;
+};
+template <bool SPLIT>
+__device__ __forceinline__ Cols cols_of(int c, int nvec) {
+  if constexpr (!SPLIT) return {c * NV, c * NV + 4};
+  const int l = c & 31, base = c - l;
+  const int a = base * NV + 4 * l;
+  return {a, a + 4 * min(32, nvec - base)};
+}
+
+__device__ __forceinline__ F8 ld8(const float* p, Cols o) {
+  const float4 a = *reinterpret_cast<const float4*>(p + o.a);
+  const float4 b = *reinterpret_cast<const float4*>(p + o.b);
   return F8{{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
 }
-__device__ __forceinline__ void st8(__nv_bfloat16* p, const F8& r) {
+template <bool SPLIT>
+__device__ __forceinline__ F8 ld8(const __nv_bfloat16* p, Cols o) {
+  if constexpr (!SPLIT) return from_bf16(*reinterpret_cast<const uint4*>(p + o.a));
+  const uint2 a = *reinterpret_cast<const uint2*>(p + o.a);
+  const uint2 b = *reinterpret_cast<const uint2*>(p + o.b);
+  return from_bf16(make_uint4(a.x, a.y, b.x, b.y));
+}
+template <bool SPLIT>
+__device__ __forceinline__ F8 ld8(const float* p, Cols o) {
+  return ld8(p, o);
+}
+__device__ __forceinline__ void st8(float* p, Cols o, const F8& r) {
+  const float2 a = halves(r.v[0]), b = halves(r.v[1]), c = halves(r.v[2]), d = halves(r.v[3]);
+  *reinterpret_cast<float4*>(p + o.a) = make_float4(a.x, a.y, b.x, b.y);
+  *reinterpret_cast<float4*>(p + o.b) = make_float4(c.x, c.y, d.x, d.y);
+}
+template <bool SPLIT>
+__device__ __forceinline__ void st8(__nv_bfloat16* p, Cols o, const F8& r) {
   uint4 u;
   uint32_t* w = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
@@ -105,12 +139,16 @@ __device__ __forceinline__ void st8(__nv_bfloat16* p, const F8& r) {
     const __nv_bfloat162 b = __float22bfloat162_rn(halves(r.v[i]));
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
-  *reinterpret_cast<uint4*>(p) = u;
+  if constexpr (!SPLIT) {
+    *reinterpret_cast<uint4*>(p + o.a) = u;
+  } else {
+    *reinterpret_cast<uint2*>(p + o.a) = make_uint2(u.x, u.y);
+    *reinterpret_cast<uint2*>(p + o.b) = make_uint2(u.z, u.w);
+  }
 }
-__device__ __forceinline__ void st8(float* p, const F8& r) {
-  const float2 a = halves(r.v[0]), b = halves(r.v[1]), c = halves(r.v[2]), d = halves(r.v[3]);
-  reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
-  reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
+template <bool SPLIT>
+__device__ __forceinline__ void st8(float* p, Cols o, const F8& r) {
+  st8(p, o, r);
 }
 
 constexpr int MAX_WARPS = 16;  // of a CTA
@@ -188,22 +226,19 @@ __device__ __forceinline__ void cp_wait(int n) {
   }
 }
 
-// One matrix's row in a ring stage: 16 bytes a vector in bf16, two pieces of 16 in FP32,
-// the first pieces of all vectors before the second ones.
-__device__ __forceinline__ void cp_row(uint4* st, int nvec, int c, const __nv_bfloat16* g) {
-  cp16(st + c, g);
+// A thread's part of a row into a ring stage that holds the row as memory does: of bf16 the
+// 16 bytes of vector c, which with split columns other lanes of the warp read; of FP32 its
+// own columns.
+__device__ __forceinline__ void cp_row(uint4* st, int c, Cols, const __nv_bfloat16* row) {
+  cp16(st + c, row + c * NV);
 }
-__device__ __forceinline__ void cp_row(uint4* st, int nvec, int c, const float* g) {
-  cp16(st + c, g);
-  cp16(st + nvec + c, g + 4);
+__device__ __forceinline__ void cp_row(uint4* st, int, Cols o, const float* row) {
+  cp16(st + o.a / 4, row + o.a);
+  cp16(st + o.b / 4, row + o.b);
 }
-__device__ __forceinline__ F8 rd_row(const uint4* st, int nvec, int c, const __nv_bfloat16*) {
-  return from_bf16(st[c]);
-}
-__device__ __forceinline__ F8 rd_row(const uint4* st, int nvec, int c, const float*) {
-  const float4 a = *reinterpret_cast<const float4*>(st + c);
-  const float4 b = *reinterpret_cast<const float4*>(st + nvec + c);
-  return F8{{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
+template <typename T, bool SPLIT>
+__device__ __forceinline__ F8 rd_row(const uint4* st, Cols o) {
+  return ld8<SPLIT>(reinterpret_cast<const T*>(st), o);
 }
 
 struct FwdK {
@@ -219,15 +254,15 @@ struct FwdK {
 
 // beta gate w_post of a vector (w_post and gate may be NULL).
 __device__ __forceinline__ F8 post_factor(const float* w_post, const float* gate, float beta,
-                                          int c) {
+                                          Cols c) {
   F8 f = splat(beta);
   if (w_post) {
-    const F8 w = ld8(w_post + c * NV);
+    const F8 w = ld8(w_post, c);
 #pragma unroll
     for (int j = 0; j < NV / 2; ++j) f.v[j] = mul2(f.v[j], w.v[j]);
   }
   if (gate) {
-    const F8 g = ld8(gate + c * NV);
+    const F8 g = ld8(gate, c);
 #pragma unroll
     for (int j = 0; j < NV / 2; ++j) f.v[j] = mul2(f.v[j], g.v[j]);
   }
@@ -239,6 +274,7 @@ template <typename RT, int V, int THREADS, bool FULL>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(const FwdK a) {
   constexpr bool KEEP = V <= 2;  // the weights in registers; else read again every row
   constexpr int R = sizeof(RT) / 2, H = NV / 2;
+  constexpr bool SPLIT = R == 2;
   extern __shared__ uint4 ring[];
   __shared__ __align__(16) float sh[2 * MAX_WARPS];
   behind();
@@ -249,11 +285,14 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(cons
   if (tid < 2 * MAX_WARPS) sh[tid] = 0.0f;
   __syncthreads();
   auto on = [&](int i) { return FULL || tid + i * nt < nvec; };
-  // this thread's first vector of the next row to copy, and of the row being worked on
-  const __nv_bfloat16* y_next = a.y + t0 * a.d + tid * NV;
-  const RT* res_next = reinterpret_cast<const RT*>(a.res) + t0 * a.d + tid * NV;
-  RT* u_out = reinterpret_cast<RT*>(a.u) + t0 * a.d + tid * NV;
-  __nv_bfloat16* n_out = a.n + t0 * a.d + tid * NV;
+  Cols at[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) at[i] = cols_of<SPLIT>(tid + i * nt, nvec);
+  // the next row to copy, and the row being worked on
+  const __nv_bfloat16* y_next = a.y + t0 * a.d;
+  const RT* res_next = reinterpret_cast<const RT*>(a.res) + t0 * a.d;
+  RT* u_out = reinterpret_cast<RT*>(a.u) + t0 * a.d;
+  __nv_bfloat16* n_out = a.n + t0 * a.d;
   int put = 0, get = 0;  // ring stages of those rows
   int left = (int)(t1 - t0);
   auto issue = [&]() {
@@ -262,8 +301,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(cons
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (on(i)) {
-          if (a.y) cp_row(st, nvec, tid + i * nt, y_next + i * nt * NV);
-          cp_row(st + nvec, nvec, tid + i * nt, res_next + i * nt * NV);
+          if (a.y) cp_row(st, tid + i * nt, at[i], y_next);
+          cp_row(st + nvec, tid + i * nt, at[i], res_next);
         }
       y_next += a.d;
       res_next += a.d;
@@ -277,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(cons
   if constexpr (KEEP) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (a.w_pre && on(i)) wp[i] = ld8(a.w_pre + (tid + i * nt) * NV);
+      if (a.w_pre && on(i)) wp[i] = ld8(a.w_pre, at[i]);
   }
   const float inv_d = 1.0f / a.d;
   int64_t seq_end = t0;  // first token past the gate row that f holds
@@ -290,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(cons
       if constexpr (KEEP) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (a.y && on(i)) f[i] = post_factor(a.w_post, gate, a.beta, tid + i * nt);
+          if (a.y && on(i)) f[i] = post_factor(a.w_post, gate, a.beta, at[i]);
       }
     }
     if (S == 1) {
@@ -298,6 +337,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(cons
       issue();
     }
     cp_wait(S > 1 ? S - 2 : 0);
+    if (SPLIT) __syncwarp();  // the warp's bf16 rows are in
     const uint4* st = ring + get * row_v;
     get = get + 1 == S ? 0 : get + 1;
     F8 u[V];
@@ -307,7 +347,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(cons
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (on(i)) {
-          y[i] = rd_row(st, nvec, tid + i * nt, a.y);
+          y[i] = rd_row<__nv_bfloat16, SPLIT>(st, at[i]);
 #pragma unroll
           for (int j = 0; j < H; ++j) s = fma2(y[i].v[j], y[i].v[j], s);
         }
@@ -318,20 +358,20 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(cons
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (on(i)) {
-          u[i] = rd_row(st + nvec, nvec, tid + i * nt, reinterpret_cast<const RT*>(a.res));
-          const F8 g = KEEP ? f[KEEP ? i : 0] : post_factor(a.w_post, gate, a.beta, tid + i * nt);
+          u[i] = rd_row<RT, SPLIT>(st + nvec, at[i]);
+          const F8 g = KEEP ? f[KEEP ? i : 0] : post_factor(a.w_post, gate, a.beta, at[i]);
 #pragma unroll
           for (int j = 0; j < H; ++j) {
             u[i].v[j] = fma2(al, u[i].v[j], mul2(mul2(g.v[j], rr), y[i].v[j]));
             s = fma2(u[i].v[j], u[i].v[j], s);
           }
-          st8(u_out + i * nt * NV, u[i]);
+          st8<SPLIT>(u_out, at[i], u[i]);
         }
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (on(i)) {
-          u[i] = rd_row(st + nvec, nvec, tid + i * nt, reinterpret_cast<const RT*>(a.res));
+          u[i] = rd_row<RT, SPLIT>(st + nvec, at[i]);
 #pragma unroll
           for (int j = 0; j < H; ++j) s = fma2(u[i].v[j], u[i].v[j], s);
         }
@@ -345,10 +385,10 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(cons
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (on(i)) {
-          F8 w = KEEP ? wp[KEEP ? i : 0] : ld8(a.w_pre + (tid + i * nt) * NV);
+          F8 w = KEEP ? wp[KEEP ? i : 0] : ld8(a.w_pre, at[i]);
 #pragma unroll
           for (int j = 0; j < H; ++j) w.v[j] = mul2(mul2(w.v[j], r2), u[i].v[j]);
-          st8(n_out + i * nt * NV, w);
+          st8<SPLIT>(n_out, at[i], w);
         }
     } else {
       if (!a.w_post) __syncthreads();  // as a statistic's barrier
@@ -382,6 +422,7 @@ template <typename RT, int V, int THREADS, bool FULL>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(const BwdK a) {
   constexpr bool KEEP = V <= 2;
   constexpr int R = sizeof(RT) / 2, H = NV / 2;
+  constexpr bool SPLIT = R == 2;
   extern __shared__ uint4 ring[];
   __shared__ float sh[2 * MAX_WARPS * 8];
   behind();
@@ -390,8 +431,11 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
   const int64_t t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
   const int S = a.stages, row_v = (2 + 2 * R) * nvec;  // a stage: dn, y, dres_out, u
   auto on = [&](int i) { return FULL || tid + i * nt < nvec; };
-  // this thread's first vector of the next row to copy, and of the row being worked on
-  const int64_t first = t0 * a.d + tid * NV;
+  Cols at[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) at[i] = cols_of<SPLIT>(tid + i * nt, nvec);
+  // the next row to copy, and the row being worked on
+  const int64_t first = t0 * a.d;
   const __nv_bfloat16 *dn_next = a.dn + first, *y_next = a.y + first;
   const RT* du_next = reinterpret_cast<const RT*>(a.du) + first;
   const RT* u_next = reinterpret_cast<const RT*>(a.u) + first;
@@ -405,13 +449,13 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (on(i)) {
-          const int c = tid + i * nt, o = i * nt * NV;
+          const int c = tid + i * nt;
           if (a.dn) {
-            cp_row(st, nvec, c, dn_next + o);
-            cp_row(st + (2 + R) * nvec, nvec, c, u_next + o);
+            cp_row(st, c, at[i], dn_next);
+            cp_row(st + (2 + R) * nvec, c, at[i], u_next);
           }
-          if (a.y) cp_row(st + nvec, nvec, c, y_next + o);
-          if (a.du) cp_row(st + 2 * nvec, nvec, c, du_next + o);
+          if (a.y) cp_row(st + nvec, c, at[i], y_next);
+          if (a.du) cp_row(st + 2 * nvec, c, at[i], du_next);
         }
       dn_next += a.d;
       y_next += a.d;
@@ -423,7 +467,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
     cp_commit();
   };
   // matrices that are not there read as zeros: no copy ever writes their part of the ring
-  if (!a.dn || !a.y || !a.du)
+  if (!a.dn || !a.y || !a.du) {
     for (int s = 0; s < S; ++s)
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -438,6 +482,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
             if (!a.dn) st[(2 + R + r) * nvec] = z;
           }
         }
+    __syncthreads();  // other threads read them
+  }
   for (int s = 0; s + 1 < S; ++s) issue();
   F8 sa[V], sb[V], f[KEEP ? V : 1], wp[KEEP ? V : 1];
   const F8 zero = splat(0.0f);
@@ -446,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
   if constexpr (KEEP) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      wp[i] = a.dn && on(i) ? ld8(a.w_pre + (tid + i * nt) * NV) : zero;
+      wp[i] = a.dn && on(i) ? ld8(a.w_pre, at[i]) : zero;
   }
   const float inv_d = 1.0f / a.d;
   const f32x2 alpha = both(a.y ? a.alpha : 1.0f);
@@ -461,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
       if constexpr (KEEP) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          f[i] = a.y && on(i) ? post_factor(a.w_post, gate, a.beta, tid + i * nt) : zero;
+          f[i] = a.y && on(i) ? post_factor(a.w_post, gate, a.beta, at[i]) : zero;
       }
     }
     if (S == 1) {
@@ -469,23 +515,23 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
       issue();
     }
     cp_wait(S > 1 ? S - 2 : 0);
+    if (SPLIT) __syncwarp();  // the warp's bf16 rows are in
     const uint4* st = ring + get * row_v;
     get = get + 1 == S ? 0 : get + 1;
     F8 dn[V], y[V], du[V], u[V];
     auto read = [&](int i) {
-      const int c = tid + i * nt;
-      dn[i] = rd_row(st, nvec, c, a.dn);
-      y[i] = rd_row(st + nvec, nvec, c, a.y);
-      du[i] = rd_row(st + 2 * nvec, nvec, c, reinterpret_cast<const RT*>(a.du));
-      u[i] = rd_row(st + (2 + R) * nvec, nvec, c, reinterpret_cast<const RT*>(a.u));
+      dn[i] = rd_row<__nv_bfloat16, SPLIT>(st, at[i]);
+      y[i] = rd_row<__nv_bfloat16, SPLIT>(st + nvec, at[i]);
+      du[i] = rd_row<RT, SPLIT>(st + 2 * nvec, at[i]);
+      u[i] = rd_row<RT, SPLIT>(st + (2 + R) * nvec, at[i]);
     };
     auto factors = [&](int i, F8& g, F8& w) {
       if constexpr (KEEP) {
         g = f[i];
         w = wp[i];
       } else {
-        g = a.y ? post_factor(a.w_post, gate, a.beta, tid + i * nt) : zero;
-        w = a.dn ? ld8(a.w_pre + (tid + i * nt) * NV) : zero;
+        g = a.y ? post_factor(a.w_post, gate, a.beta, at[i]) : zero;
+        w = a.dn ? ld8(a.w_pre, at[i]) : zero;
       }
     };
     f32x2 s[6];
@@ -536,8 +582,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
           sa[i].v[j] = fma2(x, y[i].v[j], sa[i].v[j]);
           sb[i].v[j] = fma2(dr, u[i].v[j], sb[i].v[j]);
         }
-        st8(dres_out + i * nt * NV, dres);
-        if (a.y) st8(dy_out + i * nt * NV, dy);
+        st8<SPLIT>(dres_out, at[i], dres);
+        if (a.y) st8<SPLIT>(dy_out, at[i], dy);
       }
     dres_out += a.d;
     dy_out += a.d;
@@ -545,15 +591,14 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (on(i)) {
-          const int c = tid + i * nt;
-          if (a.seq) st8(a.seq + ((int64_t)blockIdx.x + seq) * a.d + c * NV, sa[i]);
+          if (a.seq) st8(a.seq + ((int64_t)blockIdx.x + seq) * a.d, at[i], sa[i]);
           if (a.post) {
-            float* p = a.post + (int64_t)blockIdx.x * a.d + c * NV;
-            F8 v = flushed ? ld8(p) : zero;
-            const F8 g = gate ? ld8(gate + c * NV) : splat(1.0f);
+            float* p = a.post + (int64_t)blockIdx.x * a.d;
+            F8 v = flushed ? ld8(p, at[i]) : zero;
+            const F8 g = gate ? ld8(gate, at[i]) : splat(1.0f);
 #pragma unroll
             for (int j = 0; j < H; ++j) v.v[j] = fma2(g.v[j], sa[i].v[j], v.v[j]);
-            st8(p, v);
+            st8(p, at[i], v);
           }
           sa[i] = zero;
         }
@@ -563,7 +608,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
   if (a.pre)
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (on(i)) st8(a.pre + (int64_t)blockIdx.x * a.d + (tid + i * nt) * NV, sb[i]);
+      if (on(i)) st8(a.pre + (int64_t)blockIdx.x * a.d, at[i], sb[i]);
 }
 
 struct FinK {
@@ -575,13 +620,15 @@ struct FinK {
 };
 
 // Column sums of the CTAs' rows: job 0 dw_post, 1 dw_pre, 2 + s dgate row s.  A CTA takes
-// 32 columns (d is a multiple of 64), four a thread, and 32 strands of rows, which are added
-// in a fixed order.  Bound by latency: a strand has
-// some nine rows, all on their way at once.
-__global__ void __launch_bounds__(256) block_norm_bwd_finish(const FinK a) {
-  __shared__ float4 sh[8][8];
+// 32 columns (d is a multiple of 64), four a thread, and as many strands of rows as fit its
+// threads, which are added in a fixed order.  Bound by latency: 256 threads have some nine
+// rows a strand of the up to 296 CTAs of rows over 2048 columns, all on their way at once;
+// narrower rows have up to 2368 CTAs and take 1024 threads.
+constexpr int FIN_MOST = 1024;
+__global__ void __launch_bounds__(FIN_MOST) block_norm_bwd_finish(const FinK a) {
+  __shared__ float4 sh[FIN_MOST / 32][8];
   behind();
-  const int x = threadIdx.x & 7, strand = threadIdx.x >> 3;
+  const int x = threadIdx.x & 7, strand = threadIdx.x >> 3, strands = blockDim.x / 8;
   const int cols = a.d / 32;
   const int64_t job = blockIdx.x / cols;
   const int c = (int)(blockIdx.x - job * cols) * 32 + x * 4;
@@ -618,7 +665,7 @@ __global__ void __launch_bounds__(256) block_norm_bwd_finish(const FinK a) {
   };
   src += c;
 #pragma unroll 10
-  for (int64_t r = r0 + strand; r < r1; r += 32)
+  for (int64_t r = r0 + strand; r < r1; r += strands)
     add(v, *reinterpret_cast<const float4*>(src + r * a.d));
 #pragma unroll
   for (int o = 8; o < 32; o <<= 1)
@@ -627,7 +674,7 @@ __global__ void __launch_bounds__(256) block_norm_bwd_finish(const FinK a) {
   if ((strand & 3) == 0) sh[strand >> 2][x] = v;
   __syncthreads();
   if (strand == 0) {
-    for (int i = 1; i < 8; ++i) add(v, sh[i][x]);
+    for (int i = 1; i < strands / 4; ++i) add(v, sh[i][x]);
     float4* p = reinterpret_cast<float4*>(dst + c);
     float4 o = make_float4(f.x * v.x, f.y * v.y, f.z * v.z, f.w * v.w);
     if (a.accumulate) add(o, *p);
@@ -790,7 +837,8 @@ int launch_block_norm_bwd(const moe_dims& dm, const moe_norm_cfg& c, int res_typ
   f.d = dm.d;
   f.accumulate = a.accumulate;
   f.beta = a.y ? c.block_scale : 1.0f;
-  return launch_behind(block_norm_bwd_finish, (2 + seqs) * (dm.d / 32), 256, 0, st, f);
+  return launch_behind(block_norm_bwd_finish, (2 + seqs) * (dm.d / 32), ctas > 320 ? FIN_MOST : 256,
+                       0, st, f);
 }
 
 }  // namespace moe
