@@ -12,6 +12,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -52,13 +54,26 @@ def nvcc() -> str:
 
 
 def _build_one(lib: str, extra, force: bool, verbose: bool):
+    """The sources side by side (a few at a time), then one link."""
     if not force and not stale(lib):
         return
     tmp = lib + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", INCLUDE, "-o", tmp, *sources()]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.check_call(cmd)
+    flags = [f for f in NVCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, os.path.basename(s)[:-3] + ".o") for s in sources()]
+
+        def one(src, obj):
+            cmd = [nvcc(), *flags, *extra, "-I", INCLUDE, "-c", src, "-o", obj]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            subprocess.check_call(cmd)
+
+        # the largest first: they take longest
+        jobs = sorted(zip(sources(), objs), key=lambda j: -os.path.getsize(j[0]))
+        with ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as pool:
+            for r in [pool.submit(one, *j) for j in jobs]:
+                r.result()
+        subprocess.check_call([nvcc(), *NVCC_FLAGS, "-o", tmp, *objs])
     os.replace(tmp, lib)
 
 
@@ -86,10 +101,12 @@ def _build_bind(force: bool, verbose: bool):
 def build(force: bool = False, verbose: bool = False, debug: bool = True) -> str:
     """Both libraries (the debug one unless ``debug`` is False) and the binding; returns
     libmoe.so's path."""
-    _build_bind(force, verbose)
-    _build_one(LIB, [], force, verbose)
+    jobs = [(_build_one, LIB, [], force, verbose), (_build_bind, force, verbose)]
     if debug:
-        _build_one(LIB_DEBUG, ["-DMOE_DEBUG=1"], force, verbose)
+        jobs.append((_build_one, LIB_DEBUG, ["-DMOE_DEBUG=1"], force, verbose))
+    with ThreadPoolExecutor(len(jobs)) as pool:
+        for r in [pool.submit(*j) for j in jobs]:
+            r.result()
     return LIB
 
 
