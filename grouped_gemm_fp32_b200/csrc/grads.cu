@@ -272,7 +272,8 @@ __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, uint32_
 // WS < 0: data is aligned too.  A warp takes neighbouring vectors, some a lane at a time; the words
 // that a vector needs of the next one come from the next lane.
 template <typename T, int WS>
-__device__ __noinline__ void scale_vectors(const uint4* u, uint4* o, int n, uint32_t bits, float f) {
+__device__ __noinline__ void scale_vectors(const uint4* u, uint4* o, int n, uint32_t bits,
+                                           float f) {
   constexpr int BATCH = WS < 0 ? 8 : 4;
   const int lane = threadIdx.x & 31;
   int i = (threadIdx.x >> 5) * 32 * BATCH;

@@ -159,12 +159,31 @@ static int check_route(const moe_dims* dims, const moe_route_cfg* c, int type) {
   return MOE_OK;
 }
 
+// Whether every address is a multiple of `bytes` (a power of two; NULL passes).
+static bool aligned(uintptr_t bytes, std::initializer_list<const void*> p) {
+  for (const void* q : p)
+    if (reinterpret_cast<uintptr_t>(q) & (bytes - 1)) return false;
+  return true;
+}
+
+// Whether two runs of bytes share any (NULL: none).
+static bool share(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return a && b && na > 0 && nb > 0 && p < q + (uintptr_t)nb && q < p + (uintptr_t)na;
+}
+
 int moe_route_topk(const moe_dims* dims, const moe_route_cfg* cfg, int logits_type,
                    const void* logits, const float* bias, int32_t* topk_idx, float* topk_w,
                    float* probs, void* stream) {
   const int rc = check_route(dims, cfg, logits_type);
   if (rc) return rc;
   if (dims->T > 0 && (!logits || !topk_idx || !topk_w)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(logits_type == MOE_F32 ? 4 : 2, {logits}) ||
+      !aligned(4, {bias, topk_idx, topk_w, probs}))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t cells = dims->T * dims->E;  // a token may be read again after its outputs
+  if (share(logits, cells * (logits_type == MOE_F32 ? 4 : 2), probs, cells * 4))
+    return MOE_ERR_INVALID_ARG;
   return launch_route_topk(*dims, *cfg, logits_type, logits, bias, topk_idx, topk_w, probs,
                            stream);
 }
@@ -178,6 +197,11 @@ int moe_route_bwd(const moe_dims* dims, const moe_route_cfg* cfg, int logits_typ
   if (dims->T > 0 && (!logits || !topk_idx || !topk_w || !dw || !dlogits))
     return MOE_ERR_INVALID_ARG;
   if (seq_grad && seq_len < 1) return MOE_ERR_INVALID_ARG;
+  const int size = logits_type == MOE_F32 ? 4 : 2;
+  if (!aligned(size, {logits, dlogits}) || !aligned(4, {topk_idx, topk_w, dw, seq_grad}))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t bytes = dims->T * dims->E * size;
+  if (share(logits, bytes, dlogits, bytes)) return MOE_ERR_INVALID_ARG;
   return launch_route_bwd(*dims, *cfg, logits_type, logits, topk_idx, topk_w, dw, seq_grad,
                           seq_len, dlogits, stream);
 }
@@ -193,13 +217,6 @@ static int check_norm(const moe_dims* dims, const moe_norm_cfg* c) {
   return MOE_OK;
 }
 
-// 16-byte aligned, as the vector accesses of the block norms need (NULL passes).
-static bool aligned16(std::initializer_list<const void*> p) {
-  for (const void* q : p)
-    if (reinterpret_cast<uintptr_t>(q) & 15) return false;
-  return true;
-}
-
 int moe_block_norm(const moe_dims* dims, const moe_norm_cfg* cfg, int res_type, const void* y,
                    const void* res, const float* w_post, const float* gate, const float* w_pre,
                    void* res_out, void* n, void* stream) {
@@ -209,7 +226,7 @@ int moe_block_norm(const moe_dims* dims, const moe_norm_cfg* cfg, int res_type, 
   if (dims->T == 0) return MOE_OK;  // tensors without elements may be NULL
   if (!res || (w_pre == nullptr) != (n == nullptr)) return MOE_ERR_INVALID_ARG;
   if (y ? !res_out : (w_post || gate || res_out || !n)) return MOE_ERR_INVALID_ARG;
-  if (!aligned16({y, res, w_post, gate, w_pre, res_out, n})) return MOE_ERR_INVALID_ARG;
+  if (!aligned(16, {y, res, w_post, gate, w_pre, res_out, n})) return MOE_ERR_INVALID_ARG;
   NormArgs a{};
   a.y = y;
   a.res = res;
@@ -241,7 +258,7 @@ int moe_block_norm_bwd(const moe_dims* dims, const moe_norm_cfg* cfg, int res_ty
   }
   if ((dw_post && !w_post) || (dgate && !gate) || (dw_pre && !w_pre)) return MOE_ERR_INVALID_ARG;
   if (!ws || ws_bytes < norm_ws_bytes(*dims, *cfg)) return MOE_ERR_INVALID_ARG;
-  if (!aligned16({dn, dres_out, y, u, w_post, gate, w_pre, dy, dres, dw_post, dgate, dw_pre, ws}))
+  if (!aligned(16, {dn, dres_out, y, u, w_post, gate, w_pre, dy, dres, dw_post, dgate, dw_pre, ws}))
     return MOE_ERR_INVALID_ARG;
   NormArgs a{};
   a.y = y;

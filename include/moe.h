@@ -573,7 +573,8 @@ typedef struct moe_route_cfg {
  * Out:
  *   topk_idx [T, k] int32, topk_w [T, k] f32
  *   probs    [T, E]  f32  affinities that sum to 1 over a token's experts: p for
- *                    softmax, p / sum_e p for sigmoid (may be NULL)
+ *                    softmax, p / sum_e p for sigmoid (may be NULL); must not
+ *                    overlap logits
  * The choice is the one that 64-bit arithmetic makes on these logits; equal
  * scores go to the lower expert (equal group scores to the lower group).
  * Without a bias the experts rank by their logits.  A logit of -inf takes an
@@ -599,7 +600,7 @@ int moe_route_topk(const moe_dims* dims, const moe_route_cfg* cfg, int logits_ty
  *   logits   [T, E]  as given to the forward (logits_type)
  *   topk_idx, topk_w [T, k]  the forward's outputs; dw [T, k] f32
  *   seq_grad [ceil(T / seq_len), E] f32 (may be NULL: seq_len is not used)
- * Out: dlogits [T, E] of logits_type.  A topk_idx entry outside [0, E) is
+ * Out: dlogits [T, E] of logits_type, not overlapping logits.  A topk_idx entry outside [0, E) is
  * skipped.  The same inputs give the same bits. */
 int moe_route_bwd(const moe_dims* dims, const moe_route_cfg* cfg, int logits_type,
                   const void* logits, const int32_t* topk_idx, const float* topk_w,

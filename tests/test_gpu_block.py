@@ -274,3 +274,69 @@ def test_expert_parallel_with_another_router_and_clipping(nccl_one_rank):
     assert rel(clip.norm, whole.norm) <= DW_TOL and float(whole.norm) > 0.5
     for got, want in ((eb.full.dwg, ref.dwg), (eb.loc.dw1, ref.dw1), (eb.loc.dw2, ref.dw2)):
         assert rel(got, want) <= 2 * DW_TOL
+
+
+def test_operators_after_a_fork_and_join_in_a_capture():
+    """Inside a capture the operators stand behind a join of two streams, a memset and a copy,
+    and between other kernels: every replay sees what those wrote."""
+    T, E, k, d = 300, 64, 6, 256
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    src, logits, bias = r(T, E), torch.zeros(T, E, device="cuda"), 0.01 * r(E)
+    dm, rc = moe.MoeDims.of(T, d, E, k, 0, 64, 64), rcfg(SIGMOID | dict(n_group=8, topk_group=4))
+    idx, w = torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda")
+    dl, dw = torch.zeros(T, E, device="cuda"), r(T, k)
+    y, res, wn = r(T, d).bfloat16(), torch.zeros(T, d, device="cuda"), 1 + 0.1 * r(d)
+    base, u = r(T, d), torch.zeros(T, d, device="cuda")
+    n = torch.zeros(T, d, device="cuda").bfloat16()
+    grads = [torch.zeros(5000, device="cuda"), torch.zeros(77, device="cuda")]
+    clip = layer.GradClip(grads)
+    side = torch.cuda.Stream()
+
+    def step(main):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            res.copy_(base)
+            res.mul_(2.0)
+        logits.copy_(src)
+        logits.add_(0.5)
+        main.wait_stream(side)
+        idx.zero_()
+        moe.moe_route_topk(dm, rc, logits, bias, idx, w, None)
+        moe.moe_route_bwd(dm, rc, logits, idx, w, dw, None, 0, dl)
+        dl.mul_(3.0)
+        u.zero_()
+        moe.moe_block_norm(dm, moe.MoeNormCfg.of(), y, res, wn, None, wn, u, n)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            grads[1].fill_(2.0)
+        grads[0].copy_(u.view(-1)[:5000])
+        main.wait_stream(side)
+        clip.clip(1.0)
+
+    outs = [idx, w, dl, u, n, clip.norm, *grads]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(s)
+    s.synchronize()
+    want = [o.clone() for o in outs]
+    assert float(clip.norm) > 1.0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step(s)
+    for _ in range(3):
+        for o in outs + [logits, res]:
+            o.fill_(5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(map(torch.equal, outs, want))
+    src.mul_(-1.0)
+    base.add_(1.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [o.clone() for o in outs]
+    with torch.cuda.stream(s):
+        step(s)
+    s.synchronize()
+    assert all(map(torch.equal, outs, got))

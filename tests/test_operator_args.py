@@ -195,3 +195,23 @@ def test_binding_refuses_what_it_cannot_pass(monkeypatch):
         moe.GradList([torch.zeros(4, dtype=torch.float64)])
     with pytest.raises(ValueError, match="2 gradients, 1 outs"):
         moe.GradList([1, 2], [3])
+
+
+def test_routing_refuses_outputs_over_its_logits():
+    R, L = moe.MoeRouteCfg.of, _lib.load()
+    dm, cfg = moe.MoeDims.of(64, 128, 8, 2, 0, 64, 64), R()
+    near = ctypes.c_void_p(4096 + 64 * 8 * 4 - 4)      # the last of the logits
+    for out in (P, near):
+        assert L.moe_route_topk(ctypes.byref(dm), ctypes.byref(cfg), moe.MOE_F32, P, NUL, P, P,
+                                out, NUL) == INVALID
+        assert L.moe_route_bwd(ctypes.byref(dm), ctypes.byref(cfg), moe.MOE_F32, P, P, P, P, NUL,
+                               0, out, NUL) == INVALID
+    for i in range(5):         # an address between two elements
+        p = [P, NUL, P, P, ctypes.c_void_p(1 << 20)]
+        p[i] = ODD
+        assert L.moe_route_topk(ctypes.byref(dm), ctypes.byref(cfg), moe.MOE_F32, *p,
+                                NUL) == INVALID
+        p = [P, P, P, P, NUL, 0, ctypes.c_void_p(1 << 20)]
+        p[(0, 1, 2, 3, 6)[i]] = ODD
+        assert L.moe_route_bwd(ctypes.byref(dm), ctypes.byref(cfg), moe.MOE_BF16, *p,
+                               NUL) == INVALID
