@@ -299,6 +299,7 @@ int moe_grad_norm(const moe_grad* grads, int64_t n_grads, int accumulate, double
   if (rc) return rc;
   if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
   if (!sumsq || !ws || ws_bytes < grad_ws_bytes(n_grads)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(8, {sumsq, ws}) || !aligned(4, {norm})) return MOE_ERR_INVALID_ARG;
   return launch_grad_norm(grads, n_grads, accumulate, sumsq, norm, ws, stream);
 }
 
@@ -307,6 +308,7 @@ int moe_grad_clip(const moe_grad* grads, int64_t n_grads, const double* sumsq, f
   const int rc = check_grads(grads, n_grads);
   if (rc) return rc;
   if (!sumsq || !(max_norm >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(8, {sumsq}) || !aligned(4, {norm, coef})) return MOE_ERR_INVALID_ARG;
   return launch_grad_clip(grads, n_grads, sumsq, max_norm, norm, coef, stream);
 }
 
@@ -316,6 +318,7 @@ int moe_grad_clip_norm(const moe_grad* grads, int64_t n_grads, float max_norm, d
   if (rc) return rc;
   if (!sumsq || !(max_norm >= 0.0f) || !ws || ws_bytes < grad_ws_bytes(n_grads))
     return MOE_ERR_INVALID_ARG;
+  if (!aligned(8, {sumsq, ws}) || !aligned(4, {norm, coef})) return MOE_ERR_INVALID_ARG;
   return launch_grad_clip_norm(grads, n_grads, max_norm, sumsq, norm, coef, ws, stream);
 }
 

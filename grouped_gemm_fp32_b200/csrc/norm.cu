@@ -5,9 +5,14 @@
 // HBM-bound: forward y, res -> u, n; backward dn, du, y, u -> dy, dres, every
 // element once.  Persistent CTAs walk a contiguous range of rows each, a row spread
 // over the CTA's threads, eight columns a vector.  Rows come in by cp.async into a ring
-// in shared memory, several rows ahead; a thread copies and reads its own columns only,
-// so a row costs one barrier a statistic and none for its data.  The weights stay in
-// registers (rows of up to 8192 columns), and so do the backward's sums over tokens.
+// in shared memory, several rows ahead; a thread reads what it copied itself (bf16 rows
+// beside an FP32 residual: what its warp copied), so a row costs one barrier a statistic and
+// none for its data.  The weights stay in registers (rows of up to 8192 columns), and so do
+// the backward's sums over tokens.
+//
+// Measured, of the 6458 GB/s of a copy: 8192 x 4096 forward, bf16 residual, 51 us (0.81);
+// 16384 x 4096 backward with gates 140 us (0.89); with an FP32 residual 142 us (0.88) and
+// 202 us (0.93).
 //
 // The backward's statistics are one round of six row sums.  With a = dn w_pre,
 // q = beta gate w_post y, r = 1 / rms(u) and du = d + r a - c u, c = r^3 <a, u> / d:

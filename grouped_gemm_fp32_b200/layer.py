@@ -330,6 +330,8 @@ def block_forward(bb: BlockBuffers, res, w_pre, wg, bias, w1, w2, w_post=None, g
     and the gate of the layer's output (None: without).  w_next [d] f32: the next block's
     pre-norm.  Returns (res_out, n_next), n_next None without w_next."""
     dm, cfg = bb.dims, bb.norm
+    if bb.moe.train and res.data_ptr() == bb.res_out.data_ptr():
+        raise ValueError("the backward reads res again: it cannot be this block's res_out")
     if n is None:
         n = bb.n
         L.moe_block_norm(dm, cfg, None, res, None, None, w_pre, None, n, stream)

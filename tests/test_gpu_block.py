@@ -340,3 +340,11 @@ def test_operators_after_a_fork_and_join_in_a_capture():
         step(s)
     s.synchronize()
     assert all(map(torch.equal, outs, got))
+
+
+def test_block_refuses_a_residual_that_its_backward_would_miss():
+    dm, t = case(T=64)
+    bb = layer.BlockBuffers(dm, moe.MoeNormCfg.of(), train=True)
+    w = torch.ones(dm.d, device="cuda")
+    with pytest.raises(ValueError, match="cannot be this block's res_out"):
+        layer.block_forward(bb, bb.res_out, w, t["wg"], t["bias"], t["w1"], t["w2"])

@@ -387,3 +387,18 @@ def test_many_tokens_on_unaligned_views():
     assert torch.equal(i1, i2)
     ref64.within(w2, w1, 2.0 ** -20 * w1, "weights")
     ref64.within(p2, p1, 2.0 ** -20 * p1, "probs")
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("T", [50, MANY])
+@pytest.mark.parametrize("groups", [dict(), dict(n_group=4, topk_group=2)])
+def test_infinite_and_nan_biases(groups, T, score):
+    x, b, cfg = make(T, 64, 6, 12, score=score, **groups)
+    for at, v in (([3, 40, 41], INF), ([3], INF), (list(range(20, 30)), INF), ([7, 50], -INF),
+                  ([9], math.nan), ([5, 6, 30], torch.finfo(torch.float32).max)):
+        c = b.clone()
+        c[at] = v
+        _, _, idx, w, _ = call(x, c, cfg)
+        ridx, rw, _, _ = ref64.route(x, c, cfg)
+        assert torch.equal(idx, ridx), (at, v)
+        ref64.within(w, rw, 2 * (24 + 16) * 2.0 ** -23 * rw, "weights")

@@ -215,3 +215,15 @@ def test_routing_refuses_outputs_over_its_logits():
         p[(0, 1, 2, 3, 6)[i]] = ODD
         assert L.moe_route_bwd(ctypes.byref(dm), ctypes.byref(cfg), moe.MOE_BF16, *p,
                                NUL) == INVALID
+
+
+def test_gradient_calls_refuse_unaligned_results_and_workspaces():
+    L = _lib.load()
+    one = (moe.MoeGrad * 1)(moe.MoeGrad(4096, None, 4, moe.MOE_F32))
+    four = ctypes.c_void_p(4100)        # aligned for FP32, not for 64 bits
+    for sumsq, norm, ws in ((four, NUL, P), (P, ODD, P), (P, NUL, four)):
+        assert L.moe_grad_norm(one, 1, 0, sumsq, norm, ws, BIG, NUL) == INVALID
+        assert L.moe_grad_clip_norm(one, 1, 1.0, sumsq, norm, NUL, ws, BIG, NUL) == INVALID
+    assert L.moe_grad_clip_norm(one, 1, 1.0, P, NUL, ODD, P, BIG, NUL) == INVALID
+    for sumsq, norm, coef in ((four, NUL, NUL), (P, ODD, NUL), (P, NUL, ODD)):
+        assert L.moe_grad_clip(one, 1, sumsq, 1.0, norm, coef, NUL) == INVALID
