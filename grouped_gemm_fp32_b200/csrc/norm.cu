@@ -11,7 +11,7 @@
 // the backward's sums over tokens.
 //
 // Measured, of the 6458 GB/s of a copy: 8192 x 4096 forward, bf16 residual, 51 us (0.81);
-// 16384 x 4096 backward with gates 140 us (0.89); with an FP32 residual 142 us (0.88) and
+// 16384 x 4096 backward with gates 146 us (0.86); with an FP32 residual 142 us (0.88) and
 // 202 us (0.93).
 //
 // The backward's statistics are one round of six row sums.  With a = dn w_pre,
@@ -41,14 +41,15 @@ constexpr int NV = 8;             // columns per vector
 // lane on: 16384 rows of 512 columns 10.4 instead of 15.4 us, 1024 22 instead of 30, 1536 39
 // instead of 56.  The backward has more arithmetic and registers: 1536 columns 65 instead of
 // 73 us, 1984 84 instead of 90, but 768 45 instead of 42, and 2000 rows of 1024 16 instead
-// of 13.
+// of 13; and more CTAs, of which few rows feel the column sums: 2000 rows of 1984 18.7
+// instead of 20.6 us, 777 18.1 instead of 16.3.
 struct Shape {
   int v, threads, per_sm;
 };
-Shape shape_of(int d, bool bwd) {
+Shape shape_of(int64_t T, int d, bool bwd) {
   const int nvec = d / NV;
   Shape s;
-  s.v = nvec <= (bwd ? 128 : 32) ? 1 : nvec <= 1024 ? 2 : 4;
+  s.v = nvec <= (!bwd ? 32 : T < 1024 ? 256 : 128) ? 1 : nvec <= 1024 ? 2 : 4;
   s.threads = ((nvec + s.v - 1) / s.v + 31) / 32 * 32;
   s.per_sm = 512 / s.threads;
   if (s.per_sm > 16) s.per_sm = 16;
@@ -698,7 +699,7 @@ int64_t gate_rows(const moe_dims& dm, const moe_norm_cfg& c) {
 
 // CTAs of a launch over T rows and the rows each takes.
 int64_t split_rows(int64_t T, int d, bool bwd, int64_t* rows) {
-  const int64_t most = (int64_t)NB_SMS * shape_of(d, bwd).per_sm;
+  const int64_t most = (int64_t)NB_SMS * shape_of(T, d, bwd).per_sm;
   *rows = T ? (T + most - 1) / most : 1;
   return (T + *rows - 1) / *rows;
 }
@@ -736,7 +737,7 @@ int launch_rows(void (*kernel)(const K), std::atomic<uint64_t>& ready, K k, int 
 template <typename RT>
 int fwd(const FwdK& k, int64_t ctas, cudaStream_t st) {
   static std::atomic<uint64_t> ready[7];
-  const Shape s = shape_of(k.d, false);
+  const Shape s = shape_of(k.T, k.d, false);
   const int p = 1 + sizeof(RT) / 2;
   const bool full = s.v * s.threads == k.d / NV;
   if (s.v == 1)
@@ -754,7 +755,7 @@ int fwd(const FwdK& k, int64_t ctas, cudaStream_t st) {
 template <typename RT>
 int bwd(const BwdK& k, int64_t ctas, cudaStream_t st) {
   static std::atomic<uint64_t> ready[7];
-  const Shape s = shape_of(k.d, true);
+  const Shape s = shape_of(k.T, k.d, true);
   const int p = 2 + 2 * (sizeof(RT) / 2);
   const bool full = s.v * s.threads == k.d / NV;
   if (s.v == 1)
