@@ -573,6 +573,14 @@ __device__ __noinline__ double rz_f64(const LT* row, int E, float m) {
   return 1.0 / warp_sum(z);
 }
 
+// The lowest key whose score may be the last pick's: within twice an affinity's error and the
+// scores' own roundings of it.  A score of +inf has neither.
+__device__ __forceinline__ uint32_t lowest_near(uint32_t last, float two_dp) {
+  const float s = unordered(last);
+  if (last == ORD_NEG_INF) return last + 1;
+  return s == INFINITY ? last : ordered(s - (two_dp + 0x1p-22f * fabsf(s)));
+}
+
 // The picks of a token where FP32 does not settle their order, after route_token and its
 // outputs: among the experts whose keys are `least` or more, one a lane, by 64-bit scores.
 // The token's SEG lanes from `base` on hold EPL experts each, by slot in keys and ps;
@@ -598,7 +606,7 @@ __device__ __noinline__ bool refine(const RouteArgs& a, int64_t t, float m, floa
     if (lane >= o) at += v;
   }
   const int n = __shfl_sync(FULL, at, 31);
-  if (n > 32) return false;
+  if (n == 0 || n > 32) return false;  // every lane below reads an entry of the list
   at -= mine;
   __syncwarp();
   for (; bits; bits &= bits - 1) list[at++] = l * EPL + __ffs(bits) - 1;
@@ -762,8 +770,7 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, RouteS
     }
     // and the first that is not picked
     const uint32_t after = __reduce_max_sync(FULL, best.v[0]);
-    const float sl = unordered(last), margin = two_dp + 0x1p-22f * fabsf(sl);
-    const uint32_t least = last == ORD_NEG_INF ? last + 1 : ordered(sl - margin);
+    const uint32_t least = lowest_near(last, two_dp);
     if (after > ORD_NEG_INF && after >= least) {  // equal in 64 bits too?
       const int el = __shfl_sync(FULL, e, a.k - 1);
       const float xl = load1(row + el), bl = a.bias[el];
@@ -997,8 +1004,7 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8)
       near = near && !(load1(row + e) == load1(row + en) && a.bias[e] == a.bias[en] && e < en);
     }
     const uint32_t after = seg_max<SEG>(best.v[0]);
-    const float sl = unordered(last), margin = two_dp + 0x1p-22f * fabsf(sl);
-    least = last == ORD_NEG_INF ? last + 1 : ordered(sl - margin);
+    least = lowest_near(last, two_dp);
     const bool close = after > ORD_NEG_INF && after >= least;
     if (__any_sync(FULL, close)) {  // equal in 64 bits too?
       const int el = __shfl_sync(FULL, e, base + a.k - 1);

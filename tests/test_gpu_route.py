@@ -402,3 +402,22 @@ def test_infinite_and_nan_biases(groups, T, score):
         ridx, rw, _, _ = ref64.route(x, c, cfg)
         assert torch.equal(idx, ridx), (at, v)
         ref64.within(w, rw, 2 * (24 + 16) * 2.0 ** -23 * rw, "weights")
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("T", [50, MANY])
+@pytest.mark.parametrize("groups", [dict(), dict(n_group=4, topk_group=2)])
+@pytest.mark.parametrize("E", [64, 128])
+def test_picks_of_infinite_score(E, groups, T, score):
+    # fewer, exactly and more experts with a bias of +inf than the token picks, in one lane's
+    # experts, spread over all, and more than a warp of them
+    x, b, cfg = make(T, E, 6, 12, score=score, **groups)
+    step = E // 16
+    for at in ([3, 40], [0, 1, 2, 3, 4], [0, 1, 2, 3, 4, 5], list(range(E - 7, E)),
+               list(range(0, E, step)), list(range(5, 45)), list(range(E))):
+        c = b.clone()
+        c[at] = INF
+        _, _, idx, w, _ = call(x, c, cfg)
+        ridx, rw, _, _ = ref64.route(x, c, cfg)
+        assert torch.equal(idx, ridx), at
+        ref64.within(w, rw, 2 * (24 + 16) * 2.0 ** -23 * rw, "weights")
