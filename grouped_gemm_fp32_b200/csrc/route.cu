@@ -574,11 +574,12 @@ __device__ __noinline__ double rz_f64(const LT* row, int E, float m) {
 }
 
 // The lowest key whose score may be the last pick's: within twice an affinity's error and the
-// scores' own roundings of it.  A score of +inf has neither.
+// scores' own roundings of it.  A score of +inf has neither, and what ranks at -inf (taken out,
+// or of a group that is not kept) is not in question beside the lowest finite score either.
 __device__ __forceinline__ uint32_t lowest_near(uint32_t last, float two_dp) {
   const float s = unordered(last);
-  if (last == ORD_NEG_INF) return last + 1;
-  return s == INFINITY ? last : ordered(s - (two_dp + 0x1p-22f * fabsf(s)));
+  if (s == INFINITY) return last;
+  return max(ordered(s - (two_dp + 0x1p-22f * fabsf(s))), ORD_NEG_INF + 1);
 }
 
 // The picks of a token where FP32 does not settle their order, after route_token and its

@@ -421,3 +421,19 @@ def test_picks_of_infinite_score(E, groups, T, score):
         ridx, rw, _, _ = ref64.route(x, c, cfg)
         assert torch.equal(idx, ridx), at
         ref64.within(w, rw, 2 * (24 + 16) * 2.0 ** -23 * rw, "weights")
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("T", [50, MANY])
+def test_biases_of_the_lowest_value_beside_groups_that_are_not_kept(T, score):
+    # the picks after the first have the lowest finite score, as the experts of the groups that
+    # are not kept would have, of which some stand before them
+    low = torch.finfo(torch.float32).min
+    x, b, cfg = make(T, 32, 6, 13, score=score, n_group=4, topk_group=1)
+    for one in (12, 20, 31):
+        c = torch.full_like(b, low)
+        c[one] = 0.25
+        _, _, idx, w, _ = call(x, c, cfg)
+        ridx, rw, _, _ = ref64.route(x, c, cfg)
+        assert torch.equal(idx, ridx), one
+        ref64.within(w, rw, 2 * (24 + 16) * 2.0 ** -23 * rw, "weights")
