@@ -445,6 +445,15 @@ __device__ __noinline__ void refine_groups(const RouteArgs& a, const LT* row, fl
   }
 }
 
+// The error of a group's score, of its best scores b1 and b2: an affinity's error and a rounding
+// for each of its terms, and its own.  NaN where the sum of two finite scores leaves FP32.
+__device__ __forceinline__ float group_error(const RouteArgs& a, float b1, float b2,
+                                             float two_dp) {
+  const float m1 = fabsf(b1), m2 = a.group_top == 2 ? fabsf(b2) : 0.0f;
+  if (m1 + m2 < INFINITY) return two_dp + 0x1p-22f * (m1 + m2);
+  return fmaxf(m1, m2) < INFINITY ? NAN : two_dp;
+}
+
 // Gives the experts of groups that are not kept the score -inf.  two_dp: twice an
 // affinity's error; m: the largest logit, for refine_groups.
 template <typename LT, int EPL>
@@ -453,13 +462,11 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, const LT* row, f
   const int lane = threadIdx.x & 31, e0 = lane * EPL;
   const int size = a.E / a.n_group, lanes = size / EPL;
   // of the groups that this lane compares, ordered: the lowest score kept, less its error,
-  // and the highest that is not, and its error.  An affinity's error and a rounding for each
-  // of a score's terms, and its own
+  // and the highest that is not, and its error
   uint32_t low = 0xffffffffu, high = 0;
   float err = 0.0f;
   auto score = [&](float b1, float b2) {
-    const float t = a.group_top == 2 ? fabsf(b1) + fabsf(b2) : fabsf(b1);
-    err = two_dp + (t < INFINITY ? 0x1p-22f * t : 0.0f);
+    err = group_error(a, b1, b2, two_dp);
     return a.group_top == 2 ? b1 + b2 : b1;
   };
   auto clear = [&]() {
@@ -470,7 +477,7 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, const LT* row, f
   auto sort_out = [&](float mine, bool keep) {
     if (keep) low = min(low, ordered(mine - err));
     else high = max(high, ordered(mine + err));
-    if (mine != mine) high = 0xffffffffu;  // inf - inf
+    if (mine != mine || err != err) high = 0xffffffffu;  // inf - inf, or beyond FP32
   };
   if (lanes * EPL == size && (lanes & (lanes - 1)) == 0) {  // a group is 1, 2, ... 32 lanes
     float b1 = -INFINITY, b2 = -INFINITY;
@@ -928,8 +935,7 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8)
       b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
       b1 = fmaxf(b1, o1);
     }
-    const float mag = a.group_top == 2 ? fabsf(b1) + fabsf(b2) : fabsf(b1);
-    const float err = two_dp + (mag < INFINITY ? 0x1p-22f * mag : 0.0f);
+    const float err = group_error(a, b1, b2, two_dp);
     const float mine = a.group_top == 2 ? b1 + b2 : b1;
     const int at = l & -lanes;
     int before = 0;
@@ -945,7 +951,7 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8)
     uint32_t high = here && out ? ordered(mine + err) : 0;
     low = ~seg_max<SEG>(low);
     high = seg_max<SEG>(high);
-    bad |= (here && mine != mine) || !(unordered(low) > unordered(high) || high <= ORD_NEG_INF);
+    bad |= (here && (mine != mine || err != err)) || !(unordered(low) > unordered(high) || high <= ORD_NEG_INF);
   }
   uint32_t u[EPL];
 #pragma unroll

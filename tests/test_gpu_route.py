@@ -437,3 +437,23 @@ def test_biases_of_the_lowest_value_beside_groups_that_are_not_kept(T, score):
         ridx, rw, _, _ = ref64.route(x, c, cfg)
         assert torch.equal(idx, ridx), one
         ref64.within(w, rw, 2 * (24 + 16) * 2.0 ** -23 * rw, "weights")
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("T", [50, MANY])
+@pytest.mark.parametrize("E,G", [(32, 4), (64, 4), (60, 5), (128, 16), (250, 10), (256, 64)])
+def test_group_scores_beyond_fp32(E, G, T, score):
+    # two of a group's scores are finite and their sum is below FP32's lowest value, or above
+    # its highest: the groups are ordered by the sum all the same
+    x, b, cfg = make(T, E, 3, 14, score=score, n_group=G, topk_group=2)
+    low = torch.finfo(torch.float32).min
+    per = E // G
+    for sign in (1.0, -1.0):
+        c = torch.full_like(b, sign * low)
+        for g, f in ((0, 0.9), (1, 0.8), (2, 0.6), (G - 1, 0.7)):
+            c[g * per:(g + 1) * per] = sign * f * low
+        for y in (x, x.index_fill(1, torch.arange(per, device="cuda"), -INF)):
+            _, _, idx, w, _ = call(y, c, cfg)
+            ridx, rw, _, _ = ref64.route(y, c, cfg)
+            assert torch.equal(idx, ridx)
+            ref64.within(w, rw, 2 * (24 + 16) * 2.0 ** -23 * rw, "weights")
