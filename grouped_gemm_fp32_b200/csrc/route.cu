@@ -198,6 +198,14 @@ union RouteShared {
   } group;
 };
 
+// A group's score of its best scores: one that lacks a second expert ranks at -inf, also
+// where the first one's is +inf.
+template <typename F>
+__device__ __forceinline__ F group_score(const RouteArgs& a, F b1, F b2) {
+  if (a.group_top == 1) return b1;
+  return b2 == -INFINITY ? b2 : b1 + b2;
+}
+
 // A token in 64 bits: the definition itself, in little code rather than little time.
 template <typename LT>
 __device__ __noinline__ void route_token_f64(const RouteArgs& a, int64_t t, RouteShared& sh) {
@@ -246,7 +254,7 @@ __device__ __noinline__ void route_token_f64(const RouteArgs& a, int64_t t, Rout
         b2 = fmax(b2, fmin(b1, v));
         b1 = fmax(b1, v);
       }
-      of_group[g] = a.group_top == 2 ? b1 + b2 : b1;
+      of_group[g] = group_score(a, b1, b2);
     }
     __syncwarp();
 #pragma unroll 1
@@ -422,7 +430,7 @@ __device__ __noinline__ void refine_groups(const RouteArgs& a, const LT* row, fl
       b2 = fmax(fmin(b1, o1), fmax(b2, o2));
       b1 = fmax(b1, o1);
     }
-    score[i] = a.group_top == 2 ? b1 + b2 : b1;
+    score[i] = group_score(a, b1, b2);
   }
   __syncwarp();
   double* of_group = sh.group.s64;
@@ -467,7 +475,7 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, const LT* row, f
   float err = 0.0f;
   auto score = [&](float b1, float b2) {
     err = group_error(a, b1, b2, two_dp);
-    return a.group_top == 2 ? b1 + b2 : b1;
+    return group_score(a, b1, b2);
   };
   auto clear = [&]() {
     const float lo = unordered(__reduce_min_sync(FULL, low));
@@ -477,7 +485,7 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, const LT* row, f
   auto sort_out = [&](float mine, bool keep) {
     if (keep) low = min(low, ordered(mine - err));
     else high = max(high, ordered(mine + err));
-    if (mine != mine || err != err) high = 0xffffffffu;  // inf - inf, or beyond FP32
+    if (err != err) high = 0xffffffffu;
   };
   if (lanes * EPL == size && (lanes & (lanes - 1)) == 0) {  // a group is 1, 2, ... 32 lanes
     float b1 = -INFINITY, b2 = -INFINITY;
@@ -936,7 +944,7 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8)
       b1 = fmaxf(b1, o1);
     }
     const float err = group_error(a, b1, b2, two_dp);
-    const float mine = a.group_top == 2 ? b1 + b2 : b1;
+    const float mine = group_score(a, b1, b2);
     const int at = l & -lanes;
     int before = 0;
     for (int h = 0; h < a.n_group; h += lanes) {
@@ -951,7 +959,7 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8)
     uint32_t high = here && out ? ordered(mine + err) : 0;
     low = ~seg_max<SEG>(low);
     high = seg_max<SEG>(high);
-    bad |= (here && (mine != mine || err != err)) || !(unordered(low) > unordered(high) || high <= ORD_NEG_INF);
+    bad |= (here && err != err) || !(unordered(low) > unordered(high) || high <= ORD_NEG_INF);
   }
   uint32_t u[EPL];
 #pragma unroll

@@ -579,10 +579,11 @@ typedef struct moe_route_cfg {
  * scores go to the lower expert (equal group scores to the lower group).
  * Without a bias the experts rank by their logits.  A logit of -inf takes an
  * expert out (p = 0, s = -inf), a bias of -inf keeps it from being chosen, and a
- * NaN score ranks as -inf.  A pick that ranks at -inf (fewer than k experts are
- * left) has weight 0, and so have all picks of a token without any expert; the
- * picks are k distinct experts in [0, E) in every case.  A NaN or +inf logit
- * makes the weights NaN where the formulas do. */
+ * NaN score ranks as -inf, as does a group with fewer than group_top experts
+ * left.  A pick that ranks at -inf (fewer than k experts are left) has weight 0,
+ * and so have all picks of a token without any expert; the picks are k distinct
+ * experts in [0, E) in every case.  A NaN or +inf logit makes the weights NaN
+ * where the formulas do. */
 int moe_route_topk(const moe_dims* dims, const moe_route_cfg* cfg, int logits_type,
                    const void* logits, const float* bias, int32_t* topk_idx, float* topk_w,
                    float* probs, void* stream);

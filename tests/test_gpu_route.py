@@ -457,3 +457,29 @@ def test_group_scores_beyond_fp32(E, G, T, score):
             ridx, rw, _, _ = ref64.route(y, c, cfg)
             assert torch.equal(idx, ridx)
             ref64.within(w, rw, 2 * (24 + 16) * 2.0 ** -23 * rw, "weights")
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("T", [50, MANY])
+@pytest.mark.parametrize("E,G", [(32, 4), (128, 8), (60, 5), (256, 16)])
+def test_a_group_of_one_infinite_and_masked_experts_ranks_last(E, G, T, score):
+    # inf - inf as a group's score: it ranks as -inf, and topk_group groups stay all the same
+    x, b, cfg = make(T, E, 3, 15, score=score, n_group=G, topk_group=2)
+    per = E // G
+    for one in (0, per - 1, E - 1):
+        c, y = b.clone(), x.clone()
+        g = one // per
+        c[one] = INF
+        for e in range(g * per, (g + 1) * per):
+            if e != one:
+                if e % 2:
+                    c[e] = -INF
+                else:
+                    y[:, e] = -INF
+        _, _, idx, w, _ = call(y, c, cfg)
+        d = b.clone()
+        d[g * per:(g + 1) * per] = -INF             # the same choice as without the group
+        ridx, rw, _, _ = ref64.route(y, d, cfg)
+        assert torch.equal(idx, ridx), one
+        ref64.within(w, rw, 2 * (24 + 16) * 2.0 ** -23 * rw, "weights")
+        check(y, c, cfg | dict(group_top=1))
