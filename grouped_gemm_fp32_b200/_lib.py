@@ -506,7 +506,8 @@ class GradList:
             raise ValueError(f"{len(self.grads)} gradients, {len(self.outs)} outs")
         self.array = (MoeGrad * max(1, len(self.grads)))()
         self.address = ctypes.addressof(self.array)
-        dev = _types()["device"]() if self.grads else 0
+        # the calls read addresses: they have to be made on the tensors' device
+        dev = self.device = _types()["device"]() if self.grads else None
         for a, g, o in zip(self.array, self.grads, self.outs):
             a.type = _kind("gradient", g, (MOE_F32, MOE_BF16, MOE_F16))
             a.data = _need("gradient", g, g.dtype, g.numel(), dev)
@@ -516,21 +517,31 @@ class GradList:
     def __len__(self):
         return len(self.grads)
 
+    def on(self, dev):
+        """Its address and length, for a call on device ``dev``."""
+        if self.device != dev and self.device is not None:
+            raise ValueError(f"gradients: on device {self.device}, the current device is "
+                             f"cuda:{dev}")
+        return self.address, len(self.grads)
+
 
 def moe_grad_workspace_size(n_grads) -> int:
     return int(load().moe_grad_workspace_size(int(n_grads)))
 
 
 def moe_grad_norm(grads, accumulate, sumsq, norm, ws, stream=None):
-    _ck((_bound or _bind()).grad_norm(grads.address, len(grads), accumulate, sumsq, norm, ws,
-                                      *_here(stream)), "moe_grad_norm")
+    at = _here(stream)
+    _ck((_bound or _bind()).grad_norm(*grads.on(at[0]), accumulate, sumsq, norm, ws, *at),
+        "moe_grad_norm")
 
 
 def moe_grad_clip(grads, sumsq, max_norm, norm, coef, stream=None):
-    _ck((_bound or _bind()).grad_clip(grads.address, len(grads), sumsq, max_norm, norm, coef,
-                                      *_here(stream)), "moe_grad_clip")
+    at = _here(stream)
+    _ck((_bound or _bind()).grad_clip(*grads.on(at[0]), sumsq, max_norm, norm, coef, *at),
+        "moe_grad_clip")
 
 
 def moe_grad_clip_norm(grads, max_norm, sumsq, norm, coef, ws, stream=None):
-    _ck((_bound or _bind()).grad_clip_norm(grads.address, len(grads), max_norm, sumsq, norm, coef,
-                                           ws, *_here(stream)), "moe_grad_clip_norm")
+    at = _here(stream)
+    _ck((_bound or _bind()).grad_clip_norm(*grads.on(at[0]), max_norm, sumsq, norm, coef, ws,
+                                           *at), "moe_grad_clip_norm")

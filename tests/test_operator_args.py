@@ -227,3 +227,19 @@ def test_gradient_calls_refuse_unaligned_results_and_workspaces():
     assert L.moe_grad_clip_norm(one, 1, 1.0, P, NUL, ODD, P, BIG, NUL) == INVALID
     for sumsq, norm, coef in ((four, NUL, NUL), (P, ODD, NUL), (P, NUL, ODD)):
         assert L.moe_grad_clip(one, 1, sumsq, 1.0, norm, coef, NUL) == INVALID
+
+
+def test_gradient_calls_refuse_a_list_of_another_device(monkeypatch):
+    # the list holds addresses: those of another device must not reach a kernel on this one
+    _lib._types()
+    monkeypatch.setitem(_lib._TYPES, "device", lambda: -1)   # host tensors play device -1
+    lst, none = moe.GradList([torch.zeros(4)]), moe.GradList([])
+    monkeypatch.setitem(_lib._TYPES, "device", lambda: 0)
+    ws = torch.zeros(8, dtype=torch.uint8)
+    for call in (lambda g: moe.moe_grad_norm(g, 0, 16, None, ws, 0),
+                 lambda g: moe.moe_grad_clip(g, torch.zeros(1), 1.0, None, None, 0),
+                 lambda g: moe.moe_grad_clip_norm(g, 1.0, 16, None, None, ws, 0)):
+        with pytest.raises(ValueError, match="gradients: on device -1, the current device is cuda:0"):
+            call(lst)
+        with pytest.raises(ValueError, match="ws: a contiguous|sumsq: torch.float32"):
+            call(none)      # a list without tensors has no device: the next check answers
