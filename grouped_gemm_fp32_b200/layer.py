@@ -252,22 +252,29 @@ class GradClip:
     device: ``GradClip(grads)``, then ``clip(max_norm)`` every step.
 
     ``sharded``: tensors that this rank alone holds of the model's (under expert
-    parallelism the routed experts' dW); their squares are added over ``group``.
+    parallelism the routed experts' dW); their squares are added over ``group``.  Either
+    every rank of ``group`` gives a list, which is empty on a rank that holds none, or
+    none does (None): ``clip`` of a given list takes part in the group's sum.
     ``grads`` are whole on every rank (after ``dp_allreduce_grads``) and count once.
     ``outs`` / ``sharded_outs``: where the clipped gradients go (None: in place)."""
 
-    def __init__(self, grads, outs=None, sharded=(), sharded_outs=None, group=None):
+    def __init__(self, grads, outs=None, sharded=None, sharded_outs=None, group=None):
         self.whole = L.GradList(grads, outs)
-        self.shards = L.GradList(sharded, sharded_outs) if len(sharded) else None
+        self.shards = None
+        if sharded is not None:
+            import torch.distributed as dist
+            # an empty list without a process group: there is nobody to add to
+            if len(sharded) or (dist.is_available() and dist.is_initialized()):
+                self.shards = L.GradList(sharded, sharded_outs)
         self.group = group
-        every = self.whole.grads + (self.shards.grads if self.shards else [])
+        every = self.whole.grads + (self.shards.grads if self.shards is not None else [])
         if not every:
             raise ValueError("no gradients to clip")
         dev = every[0].device
         self.sumsq = torch.zeros(1, dtype=torch.float64, device=dev)
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
         self.coef = torch.zeros(1, dtype=torch.float32, device=dev)
-        n = max(len(self.whole), len(self.shards) if self.shards else 0)
+        n = max(len(self.whole), len(self.shards) if self.shards is not None else 0)
         self.ws = torch.empty(L.moe_grad_workspace_size(n), dtype=torch.uint8, device=dev)
 
     def clip(self, max_norm, stream=None):

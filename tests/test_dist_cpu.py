@@ -280,3 +280,78 @@ def test_clipping_adds_the_ranks_shards_once(world):
         p.join(timeout=60)
         assert p.exitcode == 0
     assert all(ok for _, ok in out)
+
+
+def _uneven_clip_worker(rank, world, port, q):
+    """As _clip_worker, where only rank 0 holds shards (fewer experts than ranks)."""
+    os.environ.update(MASTER_ADDR="127.0.0.1", MASTER_PORT=str(port), RANK=str(rank),
+                      WORLD_SIZE=str(world), LOCAL_RANK=str(rank))
+    sys.path.insert(0, ROOT)
+    from datetime import timedelta
+    import torch
+    import torch.distributed as dist
+    from grouped_gemm_fp32_b200 import _lib, layer
+    dist.init_process_group("gloo", rank=rank, world_size=world, timeout=timedelta(seconds=20))
+    _lib._types()["device"] = lambda: -1     # host tensors
+
+    def norm(lst, accumulate, sumsq, out, ws, stream=None):
+        v = sum(float(g.double().square().sum()) for g in lst.grads)
+        sumsq.copy_(sumsq + v if accumulate else torch.tensor([v], dtype=torch.float64))
+
+    def clip(lst, sumsq, max_norm, out, coef, stream=None):
+        f = min(1.0, max_norm / (float(sumsq.sqrt()) + 1e-6))
+        for g in lst.grads:
+            g.mul_(f)
+        if out is not None:
+            out.copy_(sumsq.sqrt())
+
+    def clip_norm(lst, max_norm, sumsq, out, coef, ws, stream=None):
+        norm(lst, 0, sumsq, None, ws)
+        clip(lst, sumsq, max_norm, out, coef)
+
+    _lib.moe_grad_norm, _lib.moe_grad_clip, _lib.moe_grad_clip_norm = norm, clip, clip_norm
+    _lib.moe_grad_workspace_size = lambda n: 256
+    shared = torch.full((5,), 2.0)
+    mine = [torch.full((3,), 4.0)] if rank == 0 else []
+    c = layer.GradClip([shared], sharded=mine)
+    try:
+        got = float(c.clip(1.0)[0])
+    except RuntimeError:            # the others' collective ran out of time
+        got = -1.0
+    want = (5 * 4.0 + 3 * 16.0) ** 0.5
+    ok = abs(got - want) < 1e-5 * want
+    ok &= bool(torch.allclose(shared, torch.full((5,), 2.0 / want), rtol=1e-5))
+    # without shards anywhere no rank waits for another
+    if rank == 0:
+        alone = torch.full((4,), 3.0)
+        ok &= abs(float(layer.GradClip([alone]).clip(1.0)[0]) - 6.0) < 1e-5
+    dist.destroy_process_group()
+    q.put((rank, ok))
+
+
+@pytest.mark.parametrize("world", [2, 3])
+def test_clipping_with_ranks_that_hold_no_shards(world):
+    ctx = mp.get_context("spawn")
+    q = ctx.Queue()
+    port = _free_port()
+    procs = [ctx.Process(target=_uneven_clip_worker, args=(r, world, port, q))
+             for r in range(world)]
+    for p in procs:
+        p.start()
+    out = [q.get(timeout=240) for _ in procs]
+    for p in procs:
+        p.join(timeout=60)
+        assert p.exitcode == 0
+    assert all(ok for _, ok in out)
+
+
+def test_clipping_of_an_empty_list_of_shards_without_a_process_group(monkeypatch):
+    import torch
+    from grouped_gemm_fp32_b200 import _lib, layer
+    monkeypatch.setitem(_lib._types(), "device", lambda: -1)
+    monkeypatch.setattr(_lib, "moe_grad_workspace_size", lambda n: 256)
+    monkeypatch.setattr(_lib, "moe_grad_clip_norm",
+                        lambda lst, m, sumsq, norm, coef, ws, stream=None: norm.fill_(6.0))
+    assert float(layer.GradClip([torch.full((4,), 3.0)], sharded=[]).clip(1.0)) == 6.0
+    with pytest.raises(ValueError, match="no gradients"):
+        layer.GradClip([], sharded=[])
