@@ -201,8 +201,14 @@ def backward(b: MoEBuffers, x, dout, w1, w2, stream=None, wg=None, gamma=None, b
 # on the layer's stream.
 
 def on_stream(stream):
-    """``torch.cuda.stream(stream)`` for a torch stream, else no change of stream."""
-    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else nullcontext()
+    """``torch.cuda.stream`` of a stream as the calls take it (a torch stream, or a handle as
+    an integer: 0 is the default stream); no change of stream for None."""
+    if stream is None:
+        return nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def dp_load_counts(counts, group=None, stream=None):

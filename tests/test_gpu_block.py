@@ -348,3 +348,19 @@ def test_block_refuses_a_residual_that_its_backward_would_miss():
     w = torch.ones(dm.d, device="cuda")
     with pytest.raises(ValueError, match="cannot be this block's res_out"):
         layer.block_forward(bb, bb.res_out, w, t["wg"], t["bias"], t["w1"], t["w2"])
+
+
+def test_exchanges_run_on_a_stream_given_by_its_handle(nccl_one_rank):
+    # every call takes a stream's handle as an integer; so do the ones with an all-reduce in them
+    s = torch.cuda.Stream()
+    for handle in (s.cuda_stream, 0):
+        with layer.on_stream(handle):
+            assert torch.cuda.current_stream().cuda_stream == handle
+    assert torch.cuda.current_stream().cuda_stream == 0
+    x, y = torch.full((1 << 24,), 0.5, device="cuda"), torch.full((77,), 2.0, device="cuda")
+    clip = layer.GradClip([y], sharded=[x])
+    torch.cuda.synchronize()
+    clip.clip(1.0, stream=s.cuda_stream)
+    s.synchronize()
+    want = (0.25 * (1 << 24) + 4.0 * 77) ** 0.5
+    assert abs(float(clip.norm) - want) <= 2.0 ** -22 * want
