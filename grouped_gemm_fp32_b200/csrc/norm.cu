@@ -18,6 +18,7 @@
 // q = beta gate w_post y, r = 1 / rms(u) and du = d + r a - c u, c = r^3 <a, u> / d:
 //   <q, du> = <q, d> + r <q, a> - c <q, u>
 // so <u, u>, <a, u>, <y, y>, <q, d>, <q, a>, <q, u> give dy's mean as well.
+#include <algorithm>
 #include <atomic>
 
 #include <cuda_bf16.h>
@@ -772,9 +773,12 @@ int bwd(const BwdK& k, int64_t ctas, cudaStream_t st) {
 
 }  // namespace
 
+// For the most CTAs that T tokens or fewer can have, so that the size grows with T (the CTAs
+// of a call do not: 296 of one row each for 296 rows of 4096 columns, 150 for 300).
 size_t norm_ws_bytes(const moe_dims& dm, const moe_norm_cfg& c) {
-  int64_t rows;
-  const int64_t ctas = split_rows(dm.T, dm.d, true, &rows);
+  int64_t ctas = 0;
+  for (int64_t T : {dm.T, std::min<int64_t>(dm.T, 1)})
+    ctas = std::max(ctas, std::min<int64_t>(dm.T, NB_SMS * shape_of(T, dm.d, true).per_sm));
   return align_up((size_t)(3 * ctas + gate_rows(dm, c)) * dm.d * sizeof(float), 256);
 }
 

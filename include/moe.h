@@ -653,7 +653,8 @@ int moe_block_norm(const moe_dims* dims, const moe_norm_cfg* cfg, int res_type, 
                    void* res_out, void* n, void* stream);
 
 /* Workspace of moe_block_norm_bwd in bytes (host-side, no counterpart on the
- * pages); 0 for invalid dims or cfg. */
+ * pages); 0 for invalid dims or cfg.  It grows with T and with the gate rows, so
+ * one for the most tokens serves fewer of the same d and seq_len. */
 size_t moe_norm_workspace_size(const moe_dims* dims, const moe_norm_cfg* cfg);
 
 /* Backward of moe_block_norm (no counterpart on the pages), from the saved y and

@@ -243,3 +243,13 @@ def test_gradient_calls_refuse_a_list_of_another_device(monkeypatch):
             call(lst)
         with pytest.raises(ValueError, match="ws: a contiguous|sumsq: torch.float32"):
             call(none)      # a list without tensors has no device: the next check answers
+
+
+@pytest.mark.parametrize("d", [64, 320, 1024, 1088, 2048, 2112, 4096, 8256, 16384])
+@pytest.mark.parametrize("L", [0, 130])
+def test_norm_workspaces_grow_with_the_tokens(d, L):
+    # one allocated for the most tokens of a run serves every smaller batch
+    cfg = moe.MoeNormCfg.of(seq_len=L)
+    sizes = [moe.moe_norm_workspace_size(moe.MoeDims.of(T, d, 8, 1, 0, 64, 64), cfg)
+             for T in [*range(0, 3000), *range(16000, 16400), *range(1 << 20, (1 << 20) + 50)]]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
