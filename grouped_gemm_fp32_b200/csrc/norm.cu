@@ -14,6 +14,10 @@
 // 16384 x 4096 backward with gates 146 us (0.86); with an FP32 residual 142 us (0.88) and
 // 202 us (0.93).
 //
+// A row's sums are means: 1 / d is taken of sums of at most 256 products (a thread's, or eight
+// lanes') before they are added up, so that rows of values up to 1e18 stay in FP32's range at
+// any width.
+//
 // The backward's statistics are one round of six row sums.  With a = dn w_pre,
 // q = beta gate w_post y, r = 1 / rms(u) and du = d + r a - c u, c = r^3 <a, u> / d:
 //   <q, du> = <q, d> + r <q, a> - c <q, u>
@@ -183,11 +187,11 @@ __device__ __forceinline__ float block_sum1(float v, float* sh, int& half) {
   return s;
 }
 
-// Six sums over the CTA.  In a warp the lanes halve the values they carry at every step
+// Six sums over the CTA, by inv_d.  In a warp the lanes halve the values they carry at every step
 // (3 + 2 + 1 + 1 + 1 shuffles where six sums take 30): lanes 4 i .. 4 i + 3 end with value
 // i (values 3 and 7 are not used).  sh [2][MAX_WARPS][8] as above; every warp then adds the
 // warps' rows and hands all six to every lane.
-__device__ __forceinline__ void block_sum6(float (&v)[6], float* sh, int& half) {
+__device__ __forceinline__ void block_mean6(float (&v)[6], float inv_d, float* sh, int& half) {
   constexpr unsigned ALL = 0xffffffffu;
   float* mine = sh + half * MAX_WARPS * 8;
   half ^= 1;
@@ -207,6 +211,7 @@ __device__ __forceinline__ void block_sum6(float (&v)[6], float* sh, int& half) 
     x[i] = keep + __shfl_xor_sync(ALL, give, 8);
   }
   float y = (up4 ? x[1] : x[0]) + __shfl_xor_sync(ALL, up4 ? x[0] : x[1], 4);
+  y *= inv_d;
   y += __shfl_xor_sync(ALL, y, 2);
   y += __shfl_xor_sync(ALL, y, 1);
   if ((lane & 3) == 0) mine[(threadIdx.x >> 5) * 8 + (lane >> 2)] = y;
@@ -364,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(cons
           for (int j = 0; j < H; ++j) s = fma2(y[i].v[j], y[i].v[j], s);
         }
       float r1 = 1.0f;
-      if (a.w_post) r1 = rsqrtf(fmaf(block_sum1(sum2(s), sh, half), inv_d, a.eps));
+      if (a.w_post) r1 = rsqrtf(block_sum1(sum2(s) * inv_d, sh, half) + a.eps);
       const f32x2 rr = both(r1), al = both(a.alpha);
       s = both(0.0f);
 #pragma unroll
@@ -391,9 +396,9 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_kernel(cons
     // a copy refills the stage of the row before this one: every thread has passed a
     // barrier since it read that
     if (a.n) {
-      const float ss = block_sum1(sum2(s), sh, half);
+      const float ss = block_sum1(sum2(s) * inv_d, sh, half);
       if (S > 1) issue();
-      const f32x2 r2 = both(rsqrtf(fmaf(ss, inv_d, a.eps)));
+      const f32x2 r2 = both(rsqrtf(ss + a.eps));
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (on(i)) {
@@ -569,14 +574,13 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
     float sum[6];
 #pragma unroll
     for (int j = 0; j < 6; ++j) sum[j] = sum2(s[j]);
-    block_sum6(sum, sh, half);
+    block_mean6(sum, inv_d, sh, half);
     // the stage of the row before this one: every thread has passed a barrier since it read it
     if (S > 1) issue();
-    const float r2 = a.dn ? rsqrtf(fmaf(sum[0], inv_d, a.eps)) : 0.0f;
-    const float c2 = r2 * r2 * r2 * sum[1] * inv_d;
-    const float r1 = a.w_post ? rsqrtf(fmaf(sum[2], inv_d, a.eps)) : 1.0f;
-    const float c1 =
-        a.w_post ? r1 * r1 * r1 * inv_d * (sum[3] + r2 * sum[4] - c2 * sum[5]) : 0.0f;
+    const float r2 = a.dn ? rsqrtf(sum[0] + a.eps) : 0.0f;
+    const float c2 = r2 * r2 * r2 * sum[1];
+    const float r1 = a.w_post ? rsqrtf(sum[2] + a.eps) : 1.0f;
+    const float c1 = a.w_post ? r1 * r1 * r1 * (sum[3] + r2 * sum[4] - c2 * sum[5]) : 0.0f;
     const f32x2 r1p = both(r1), r2p = both(r2), c1n = both(-c1), c2n = both(-c2);
 #pragma unroll
     for (int i = 0; i < V; ++i)

@@ -646,8 +646,8 @@ typedef struct moe_norm_cfg {
  * Out:
  *   res_out [T, d] res_type = u (may be res itself)
  *   n     [T, d] bf16, the next block's input; NULL with w_pre NULL: no pre-norm
- * n is computed from u before u is rounded to res_type.  FP32 throughout: rows of
- * |values| below 1e18.  Requires d <= 16384 and 16-byte aligned tensors. */
+ * n is computed from u before u is rounded to res_type.  FP32 throughout: |y| and
+ * |u| below 1e18.  Requires d <= 16384 and 16-byte aligned tensors. */
 int moe_block_norm(const moe_dims* dims, const moe_norm_cfg* cfg, int res_type, const void* y,
                    const void* res, const float* w_post, const float* gate, const float* w_pre,
                    void* res_out, void* n, void* stream);
@@ -673,6 +673,7 @@ size_t moe_norm_workspace_size(const moe_dims* dims, const moe_norm_cfg* cfg);
  *   dy    [T, d] bf16; dres [T, d] res_type (may be dres_out itself)
  *   dw_post, dw_pre [d] f32, dgate as gate, f32: written, or added to when
  *         accumulate != 0; each may be NULL (not wanted)
+ * FP32 throughout: |y|, |beta gate w_post y|, |u|, |dn w_pre| and |dres_out| below 1e18.
  * Sums over tokens run in a fixed order: the same inputs give the same bits.
  * Two calls on one workspace must not overlap on the GPU. */
 int moe_block_norm_bwd(const moe_dims* dims, const moe_norm_cfg* cfg, int res_type,

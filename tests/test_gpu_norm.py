@@ -242,3 +242,28 @@ def test_streams_and_graphs():
     torch.cuda.synchronize()
     for ref, r in ((o, got[0]), (oj, got[1])):
         assert all(torch.equal(ref[k], r[k]) for k in NAMES)
+
+
+@pytest.mark.parametrize("rt", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 4096, 4160, 16384])
+def test_rows_of_the_largest_values(d, rt):
+    # every value just below 1e18: the squares' sum over a row leaves FP32, their mean does not
+    T = 5
+    i = inputs(T, d, rt, 1, seed=23)
+    big = 0.99e18
+    for n in ("y", "res"):
+        i[n] = (big * i[n].float().sign()).to(i[n].dtype)
+    i["gate"] = i["gate"].clamp(-1, 1)
+    i["w_post"] = i["w_post"].clamp(0.3, 0.9)
+    check_fwd(i, (0.0, 1.0, 0))
+    check_fwd(i, (0.5, 0.5, 0), post=False)
+    check_fwd(i, (1.0, 0.7, 0), y=False)
+    # of the backward the sums alone: gradients along a row's own direction, where the
+    # projection takes nearly all, have their own test
+    o = bwd(i, moe.MoeNormCfg.of(EPS, 1.0, 0.7))
+    ref = ref64.block_norm_bwd(i["dn"], i["du"], i["y"], i["res"], i["w_post"], i["gate"],
+                               i["w_pre"], EPS, 1.0, 0.7, 0)
+    for k in ("dres", "dw_post", "dgate", "dw_pre"):
+        v, mag = ref[k]
+        tol = E * mag if k == "dres" else (E + (T / 64 + 64) * U) * mag
+        within(o[k], v, tol + HALF[o[k].dtype] * (v.abs() + tol) + ref64.TINY[o[k].dtype], k)
