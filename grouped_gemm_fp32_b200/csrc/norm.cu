@@ -18,10 +18,13 @@
 // lanes') before they are added up, so that rows of values up to 1e18 stay in FP32's range at
 // any width.
 //
-// The backward's statistics are one round of six row sums.  With a = dn w_pre,
-// q = beta gate w_post y, r = 1 / rms(u) and du = d + r a - c u, c = r^3 <a, u> / d:
-//   <q, du> = <q, d> + r <q, a> - c <q, u>
-// so <u, u>, <a, u>, <y, y>, <q, d>, <q, a>, <q, u> give dy's mean as well.
+// The backward's statistics are one round of six row sums.  With a = dn w_pre, r2 = 1 / rms(u),
+// uh = r2 u, m2 = mean(a uh), v = dres_out + r2 (a - m2 uh) the gradient of u, and with
+// g = beta gate w_post, q = g y, r1 = 1 / rms(y), yh = r1 y, m1 = mean(g v yh):
+//   dy = r1 (g v - m1 yh),   m1 = r1 (mean(q dres_out) + r2 (mean(q a) - m2 r2 mean(q u)))
+// so u u, a u, y y, q dres_out, q a and q u are all that is summed.  Factors r1^3 and r2^3 in
+// place of uh and yh would save two products, and leave FP32's range for rows from 1e13 on and
+// below 1e-12.
 #include <algorithm>
 #include <atomic>
 
@@ -578,10 +581,12 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
     // the stage of the row before this one: every thread has passed a barrier since it read it
     if (S > 1) issue();
     const float r2 = a.dn ? rsqrtf(sum[0] + a.eps) : 0.0f;
-    const float c2 = r2 * r2 * r2 * sum[1];
     const float r1 = a.w_post ? rsqrtf(sum[2] + a.eps) : 1.0f;
-    const float c1 = a.w_post ? r1 * r1 * r1 * (sum[3] + r2 * sum[4] - c2 * sum[5]) : 0.0f;
-    const f32x2 r1p = both(r1), r2p = both(r2), c1n = both(-c1), c2n = both(-c2);
+    // the means of a uh and of g v yh
+    const float m2 = r2 * sum[1];
+    const float m1 =
+        a.w_post ? r1 * fmaf(r2, fmaf(-m2, r2 * sum[5], sum[4]), sum[3]) : 0.0f;
+    const f32x2 r1p = both(r1), r2p = both(r2), m1n = both(-m1), m2n = both(-m2);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (on(i)) {
@@ -590,13 +595,12 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
         factors(i, g, w);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-          const f32x2 dr = mul2(dn[i].v[j], r2p);  // dn / rms(u)
-          const f32x2 v = fma2(dr, w.v[j], fma2(c2n, u[i].v[j], du[i].v[j]));
+          const f32x2 uh = mul2(u[i].v[j], r2p), yh = mul2(y[i].v[j], r1p);
+          const f32x2 v = fma2(r2p, fma2(m2n, uh, mul2(dn[i].v[j], w.v[j])), du[i].v[j]);
           dres.v[j] = mul2(alpha, v);
-          const f32x2 x = mul2(r1p, v);
-          dy.v[j] = fma2(g.v[j], x, mul2(c1n, y[i].v[j]));
-          sa[i].v[j] = fma2(x, y[i].v[j], sa[i].v[j]);
-          sb[i].v[j] = fma2(dr, u[i].v[j], sb[i].v[j]);
+          dy.v[j] = mul2(r1p, fma2(m1n, yh, mul2(g.v[j], v)));
+          sa[i].v[j] = fma2(v, yh, sa[i].v[j]);
+          sb[i].v[j] = fma2(dn[i].v[j], uh, sb[i].v[j]);
         }
         st8<SPLIT>(dres_out, at[i], dres);
         if (a.y) st8<SPLIT>(dy_out, at[i], dy);

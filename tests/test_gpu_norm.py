@@ -267,3 +267,31 @@ def test_rows_of_the_largest_values(d, rt):
         v, mag = ref[k]
         tol = E * mag if k == "dres" else (E + (T / 64 + 64) * U) * mag
         within(o[k], v, tol + HALF[o[k].dtype] * (v.abs() + tol) + ref64.TINY[o[k].dtype], k)
+
+
+@pytest.mark.parametrize("rt", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d", [512, 4160, 8256])
+@pytest.mark.parametrize("su,sy,sdn,eps", [(1e13, 1.0, 1.0, 1e-6), (1.0, 1e13, 1.0, 1e-6),
+                                           (1e15, 1e15, 1.0, 1e-6), (1e16, 1e17, 1e-6, 1e-6),
+                                           (1e17, 1e16, 1e-6, 1e-6), (1e17, 1e17, 1e-3, 1e-6),
+                                           (1e-15, 1e-15, 1.0, 1e-30), (0.0, 1.0, 1.0, 1e-30),
+                                           (1.0, 0.0, 1.0, 1e-30), (0.0, 0.0, 1.0, 1e-30)])
+def test_backward_of_large_and_small_rows(su, sy, sdn, eps, d, rt):
+    # the projections on u and y are as large as the terms they are taken from, whatever the
+    # rows' size: no power of 1 / rms may leave FP32 on the way
+    T = 70
+    i = inputs(T, d, rt, 1, seed=21)
+    i["res"] = (i["res"].float() * su).to(rt)
+    i["y"] = (i["y"].float().clamp(-8, 8) * sy).to(BF)
+    for n in ("dn", "du"):
+        i[n] = (i[n].float() * sdn).to(i[n].dtype)
+    # along u and y, so that the projections take most of it away
+    i["dn"] = (i["dn"].float() + sdn * i["res"].float() / max(su, 1e-30) / 3).to(BF)
+    cfg = moe.MoeNormCfg.of(eps, 0.9, 0.7)
+    o = bwd(i, cfg)
+    ref = ref64.block_norm_bwd(i["dn"], i["du"], i["y"], i["res"], i["w_post"], i["gate"],
+                               i["w_pre"], eps, 0.9, 0.7, 0)
+    for k in NAMES:
+        v, mag = ref[k]
+        tol = E * mag if k in ("dy", "dres") else (E + (T / 64 + 64) * U) * mag
+        within(o[k], v, tol + HALF[o[k].dtype] * (v.abs() + tol) + ref64.TINY[o[k].dtype], k)
