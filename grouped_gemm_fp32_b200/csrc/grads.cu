@@ -340,6 +340,28 @@ __device__ void chunk_scale(const void* data, void* out, int64_t i0, int64_t i1,
   for (int64_t i = v1 + threadIdx.x; i < i1; i += GL_THREADS) from_f32(o + i, to_f32(p[i]) * f);
 }
 
+// All chunks with a factor below FP32's normal range, which would lose its bits there.
+template <typename T>
+__device__ void chunk_scale_f64(const void* data, void* out, int64_t i0, int64_t i1,
+                                             double f) {
+  const T* p = reinterpret_cast<const T*>(data);
+  T* o = reinterpret_cast<T*>(out);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += GL_THREADS)
+    from_f32(o + i, (float)(to_f32(p[i]) * f));
+}
+
+template <int N>
+__device__ __noinline__ void scale_f64(const GradTable<N>& tb, double f) {
+  for (int64_t c = blockIdx.x; c < tb.chunks; c += gridDim.x) {
+    const int k = find(tb, c);
+    const GradEnt& e = tb.e[k];
+    const int64_t i0 = (c - e.chunk0) * tb.chunk, i1 = min(i0 + tb.chunk, e.n);
+    if (tb.type[k] == MOE_F32) chunk_scale_f64<float>(e.data, e.out, i0, i1, f);
+    else if (tb.type[k] == MOE_BF16) chunk_scale_f64<__nv_bfloat16>(e.data, e.out, i0, i1, f);
+    else chunk_scale_f64<__half>(e.data, e.out, i0, i1, f);
+  }
+}
+
 // parts > 0: the sum of squares is that of the norm launches' partial sums, which every
 // CTA adds up for itself, and is written to sumsq; otherwise sumsq is given.  The chunks
 // are taken in the reverse of the norm's order: what it read last may still be in the L2.
@@ -356,6 +378,10 @@ __global__ void __launch_bounds__(GL_THREADS, 4)
     if (parts > 0) *sumsq = ss;
     if (norm) *norm = (float)nm;
     if (coef) *coef = f;
+  }
+  if (q < 0x1p-126 && q > 0.0) {
+    scale_f64(tb, q);
+    return;
   }
   for (int64_t r = blockIdx.x; r < tb.chunks; r += gridDim.x) {
     const int64_t c = tb.chunks - 1 - r;

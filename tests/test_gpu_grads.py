@@ -207,3 +207,27 @@ def test_one_non_finite_element_in_a_long_run(t, bad):
         moe.moe_grad_norm(moe.GradList([x]), 0, s["sumsq"], s["norm"], s["ws"])
         got = float(s["norm"])
         assert math.isnan(got) if math.isnan(bad) else got == math.inf
+
+
+@pytest.mark.parametrize("t,v,max_norm", [(F32, 3e38, 1e-3), (BF, 3e38, 1e-3), (F32, 3e37, 1e-7),
+                                          (F32, 1.5, 1e-37), (BF, 1.5, 1e-37), (F32, 2e30, 1e-38),
+                                          (F32, 3e38, 1.2e-38)])
+def test_a_factor_below_fp32_normal_range(t, v, max_norm):
+    # max_norm / norm is a subnormal number of FP32, or 0 there; the clipped elements are
+    # ordinary ones, rounded once
+    for n in (7, 100_001):
+        g = torch.full((n,), v, device="cuda").to(t)
+        g[::3] *= -0.5
+        norm = math.sqrt(float(g.double().square().sum()))
+        q = max_norm / (norm + 1e-6)
+        for out in (torch.full_like(g, 7.0), None):
+            x = g.clone()
+            lst = moe.GradList([x[:n // 2], x[n // 2:]],
+                               None if out is None else [out[:n // 2], out[n // 2:]])
+            s = state(lst)
+            moe.moe_grad_clip_norm(lst, max_norm, s["sumsq"], s["norm"], s["coef"], s["ws"])
+            r = g.double() * q
+            within(x if out is None else out, r,
+                   (4 * U + HALF[t] * (1 + 4 * U)) * r.abs() + TINY[t], "clipped")
+            assert abs(float(s["coef"]) - q) <= 2 * U * q + 2.0 ** -150
+        assert out is not None or torch.isfinite(x).all()
