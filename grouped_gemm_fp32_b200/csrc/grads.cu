@@ -372,7 +372,8 @@ __global__ void __launch_bounds__(GL_THREADS, 4)
   behind();
   const double ss = parts > 0 ? sum_parts(part, parts) : *sumsq;
   const double nm = sqrt(ss);
-  const double q = (double)max_norm / (nm + 1e-6);
+  // no limit: no clipping, whatever the norm
+  const double q = max_norm == INFINITY ? 1.0 : (double)max_norm / (nm + 1e-6);
   const float f = q >= 1.0 ? 1.0f : (float)q;  // a NaN stays one
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     if (parts > 0) *sumsq = ss;

@@ -715,7 +715,8 @@ int moe_grad_norm(const moe_grad* grads, int64_t n_grads, int accumulate, double
  * (device, each may be NULL) are written, rounded to FP32; a factor below FP32's
  * normal range is applied in 64 bits.  Tensors clipped in place are left alone
  * when coef = 1.  A sumsq that is not finite gives the formula's coef: 0 for
- * an infinite norm, NaN for a NaN.  max_norm >= 0 (infinity: never clips). */
+ * an infinite norm, NaN for a NaN.  max_norm >= 0 (infinity: coef = 1 for any
+ * norm). */
 int moe_grad_clip(const moe_grad* grads, int64_t n_grads, const double* sumsq, float max_norm,
                   float* norm, float* coef, void* stream);
 

@@ -231,3 +231,19 @@ def test_a_factor_below_fp32_normal_range(t, v, max_norm):
                    (4 * U + HALF[t] * (1 + 4 * U)) * r.abs() + TINY[t], "clipped")
             assert abs(float(s["coef"]) - q) <= 2 * U * q + 2.0 ** -150
         assert out is not None or torch.isfinite(x).all()
+
+
+@pytest.mark.parametrize("t", [F32, BF, F16])
+@pytest.mark.parametrize("bad", [math.inf, math.nan, 1.0])
+def test_an_infinite_limit_never_clips(bad, t):
+    x = rand(50_000, t, 3)
+    x[777] = bad
+    y = x.clone()
+    for outs in ([torch.zeros_like(x)], None):
+        lst = moe.GradList([x], outs)
+        s = state(lst)
+        moe.moe_grad_clip_norm(lst, math.inf, s["sumsq"], s["norm"], s["coef"], s["ws"])
+        assert float(s["coef"]) == 1.0
+        assert math.isfinite(float(s["norm"])) == (bad == 1.0)
+        for got in (x, *(outs or [])):
+            assert torch.equal(got.nan_to_num(-7.0, 9.0), y.nan_to_num(-7.0, 9.0))
