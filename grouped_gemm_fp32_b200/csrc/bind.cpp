@@ -175,8 +175,11 @@ PyObject* run(Args& a, F f) {
 
 using Fast = PyObject* const*;
 
+// Sequences of L of T tokens.
+int64_t sequences(int64_t T, int64_t L) { return T > 0 ? (T - 1) / L + 1 : 0; }
+
 int64_t gate_rows(const moe_dims* d, const moe_norm_cfg* c) {
-  const int64_t r = c->seq_len > 0 ? (d->T + c->seq_len - 1) / c->seq_len : 1;
+  const int64_t r = c->seq_len > 0 ? sequences(d->T, c->seq_len) : 1;
   return r > 1 ? r : 1;
 }
 
@@ -233,7 +236,7 @@ PyObject* route_bwd(PyObject*, Fast args, Py_ssize_t n) {
     a.at = 7;
     const int64_t L = a.integer();
     const bool seq = args[6] != Py_None && L > 0;
-    const int64_t rows = seq ? (d->T + L - 1) / L : 0;
+    const int64_t rows = seq ? sequences(d->T, L) : 0;
     a.at = 2;
     void* logits = a.tensor("logits", kind, d->T * d->E);
     void* idx = a.tensor("topk_idx", I32, d->T * d->k);

@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(FIN_MOST) block_norm_bwd_finish(const FinK a) 
 }
 
 int64_t gate_rows(const moe_dims& dm, const moe_norm_cfg& c) {
-  return c.seq_len && dm.T ? (dm.T + c.seq_len - 1) / c.seq_len : 1;
+  return c.seq_len && dm.T ? (dm.T - 1) / c.seq_len + 1 : 1;
 }
 
 // CTAs of a launch over T rows and the rows each takes.

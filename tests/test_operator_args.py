@@ -253,3 +253,20 @@ def test_norm_workspaces_grow_with_the_tokens(d, L):
     sizes = [moe.moe_norm_workspace_size(moe.MoeDims.of(T, d, 8, 1, 0, 64, 64), cfg)
              for T in [*range(0, 3000), *range(16000, 16400), *range(1 << 20, (1 << 20) + 50)]]
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.parametrize("L", [5, 1 << 40, (1 << 63) - 4, (1 << 63) - 1])
+def test_sequences_longer_than_the_tokens_are_one_row(monkeypatch, L):
+    # T + L - 1 would leave 64 bits
+    for T in (1, 2, 5):
+        dm = moe.MoeDims.of(T, 128, 8, 2, 0, 64, 64)
+        size = lambda n: moe.moe_norm_workspace_size(dm, moe.MoeNormCfg.of(seq_len=n))  # noqa: E731
+        assert size(L) == size(0)
+    _lib._types()
+    monkeypatch.setitem(_lib._TYPES, "device", lambda: -1)     # host tensors; no call is made
+    x = torch.zeros(5, 8)
+    with pytest.raises(ValueError, match="seq_grad: shape .* 8 needed"):
+        moe.moe_route_bwd(dm, moe.MoeRouteCfg.of(), x, 16, 16, 16, torch.zeros(7), L, x, 0)
+    with pytest.raises(ValueError, match="gate: shape .* 128 needed"):
+        moe.moe_block_norm(dm, moe.MoeNormCfg.of(seq_len=L), 16, torch.zeros(5, 128), 16,
+                           torch.zeros(1), 16, 16, 16, 0)
