@@ -345,6 +345,9 @@ def block_forward(bb: BlockBuffers, res, w_pre, wg, bias, w1, w2, w_post=None, g
     dm, cfg = bb.dims, bb.norm
     if bb.moe.train and res.data_ptr() == bb.res_out.data_ptr():
         raise ValueError("the backward reads res again: it cannot be this block's res_out")
+    if bb.moe.train and n is not None and w_next is not None and \
+            n.data_ptr() == bb.n_next.data_ptr():
+        raise ValueError("the backward reads n again: it cannot be this block's n_next")
     if n is None:
         n = bb.n
         L.moe_block_norm(dm, cfg, None, res, None, None, w_pre, None, n, stream)

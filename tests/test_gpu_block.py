@@ -364,3 +364,23 @@ def test_exchanges_run_on_a_stream_given_by_its_handle(nccl_one_rank):
     s.synchronize()
     want = (0.25 * (1 << 24) + 4.0 * 77) ** 0.5
     assert abs(float(clip.norm) - want) <= 2.0 ** -22 * want
+
+
+def test_block_refuses_an_input_that_its_backward_would_miss():
+    # n_next is written by the forward; the backward reads n again
+    dm, t = case(T=64)
+    w = torch.ones(dm.d, device="cuda")
+    res = torch.randn(dm.T, dm.d, device="cuda").bfloat16()
+    args = (res, None, t["wg"], t["bias"], t["w1"], t["w2"])
+    bb = layer.BlockBuffers(dm, moe.MoeNormCfg.of(), train=True)
+    bb.n_next.normal_()
+    with pytest.raises(ValueError, match="cannot be this block's n_next"):
+        layer.block_forward(bb, *args, w_next=w, n=bb.n_next)
+    layer.block_forward(bb, *args, n=bb.n_next)          # not written: as any other tensor
+    # without a backward one set of buffers serves a run of blocks
+    run = layer.BlockBuffers(dm, moe.MoeNormCfg.of())
+    run.n_next.copy_(bb.n_next)
+    other = layer.BlockBuffers(dm, moe.MoeNormCfg.of())
+    want = layer.block_forward(other, *args, w_next=w, n=run.n_next.clone())
+    got = layer.block_forward(run, *args, w_next=w, n=run.n_next)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
