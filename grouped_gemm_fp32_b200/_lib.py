@@ -395,12 +395,13 @@ _bound = None
 def _types():
     if not _TYPES:
         import torch
-        _TYPES.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16})
         # the same numbers without a Stream object and the lazy start of CUDA on the way
         # (3 us less a call); a torch without the call keeps to the public one
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _TYPES.update(device=torch.cuda.current_device,
-                      stream=raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+        # all at once: another thread may look at the table meanwhile
+        _TYPES.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16,
+                       "device": torch.cuda.current_device,
+                       "stream": raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)})
     return _TYPES
 
 

@@ -270,3 +270,14 @@ def test_sequences_longer_than_the_tokens_are_one_row(monkeypatch, L):
     with pytest.raises(ValueError, match="gate: shape .* 128 needed"):
         moe.moe_block_norm(dm, moe.MoeNormCfg.of(seq_len=L), 16, torch.zeros(5, 128), 16,
                            torch.zeros(1), 16, 16, 16, 0)
+
+
+def test_first_calls_of_two_threads_find_a_whole_table(monkeypatch):
+    # a second thread that comes in while the first fills the table must not find half of it
+    class Table(dict):
+        def update(self, *a, **kw):
+            super().update(*a, **kw)
+            assert {torch.float32, torch.bfloat16, torch.float16, "device", "stream"} <= set(self)
+
+    monkeypatch.setattr(_lib, "_TYPES", Table())
+    assert _lib._types()[torch.bfloat16] == moe.MOE_BF16 and _lib._TYPES
