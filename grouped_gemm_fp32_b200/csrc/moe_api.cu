@@ -166,10 +166,26 @@ static bool aligned(uintptr_t bytes, std::initializer_list<const void*> p) {
   return true;
 }
 
-// Whether two runs of bytes share any (NULL: none).
-static bool share(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-  return a && b && na > 0 && nb > 0 && p < q + (uintptr_t)nb && q < p + (uintptr_t)na;
+// A tensor's bytes (NULL: none).
+struct Span {
+  const void* p;
+  int64_t n;
+};
+static bool share(const Span& a, const Span& b) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+  return p && q && a.n > 0 && b.n > 0 && p < q + (uintptr_t)b.n && q < p + (uintptr_t)a.n;
+}
+// Whether an output shares bytes with an input or with another output.  rows: with an input
+// that is the very same tensor it may (a row is read before it is written).
+static bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins,
+                  bool rows = false) {
+  for (const Span& o : outs) {
+    for (const Span& i : ins)
+      if (share(o, i) && !(rows && o.p == i.p && o.n == i.n)) return true;
+    for (const Span& u : outs)
+      if (&u < &o && share(o, u)) return true;
+  }
+  return false;
 }
 
 int moe_route_topk(const moe_dims* dims, const moe_route_cfg* cfg, int logits_type,
@@ -181,8 +197,10 @@ int moe_route_topk(const moe_dims* dims, const moe_route_cfg* cfg, int logits_ty
   if (!aligned(logits_type == MOE_F32 ? 4 : 2, {logits}) ||
       !aligned(4, {bias, topk_idx, topk_w, probs}))
     return MOE_ERR_INVALID_ARG;
-  const int64_t cells = dims->T * dims->E;  // a token may be read again after its outputs
-  if (share(logits, cells * (logits_type == MOE_F32 ? 4 : 2), probs, cells * 4))
+  // a token may be read again after its outputs
+  const int64_t cells = dims->T * dims->E, picks = dims->T * dims->k;
+  if (clash({{topk_idx, picks * 4}, {topk_w, picks * 4}, {probs, cells * 4}},
+            {{logits, cells * (logits_type == MOE_F32 ? 4 : 2)}, {bias, dims->E * 4}}))
     return MOE_ERR_INVALID_ARG;
   return launch_route_topk(*dims, *cfg, logits_type, logits, bias, topk_idx, topk_w, probs,
                            stream);
@@ -200,8 +218,12 @@ int moe_route_bwd(const moe_dims* dims, const moe_route_cfg* cfg, int logits_typ
   const int size = logits_type == MOE_F32 ? 4 : 2;
   if (!aligned(size, {logits, dlogits}) || !aligned(4, {topk_idx, topk_w, dw, seq_grad}))
     return MOE_ERR_INVALID_ARG;
-  const int64_t bytes = dims->T * dims->E * size;
-  if (share(logits, bytes, dlogits, bytes)) return MOE_ERR_INVALID_ARG;
+  const int64_t cells = dims->T * dims->E, picks = dims->T * dims->k;
+  const int64_t seqs = seq_grad && dims->T ? (dims->T - 1) / seq_len + 1 : 0;
+  if (clash({{dlogits, cells * size}},
+            {{logits, cells * size}, {topk_idx, picks * 4}, {topk_w, picks * 4}, {dw, picks * 4},
+             {seq_grad, seqs * dims->E * 4}}))
+    return MOE_ERR_INVALID_ARG;
   return launch_route_bwd(*dims, *cfg, logits_type, logits, topk_idx, topk_w, dw, seq_grad,
                           seq_len, dlogits, stream);
 }
@@ -227,6 +249,12 @@ int moe_block_norm(const moe_dims* dims, const moe_norm_cfg* cfg, int res_type, 
   if (!res || (w_pre == nullptr) != (n == nullptr)) return MOE_ERR_INVALID_ARG;
   if (y ? !res_out : (w_post || gate || res_out || !n)) return MOE_ERR_INVALID_ARG;
   if (!aligned(16, {y, res, w_post, gate, w_pre, res_out, n})) return MOE_ERR_INVALID_ARG;
+  const int64_t cells = dims->T * dims->d, row = dims->d * 4, size = res_type == MOE_F32 ? 4 : 2;
+  const int64_t gates = cfg->seq_len ? (dims->T - 1) / cfg->seq_len + 1 : 1;
+  const Span out = {res_out, cells * size}, normed = {n, cells * 2};
+  if (clash({out, normed}, {{y, cells * 2}, {res, cells * size}}, true) ||
+      clash({out, normed}, {{w_post, row}, {gate, gates * row}, {w_pre, row}}))
+    return MOE_ERR_INVALID_ARG;
   NormArgs a{};
   a.y = y;
   a.res = res;
@@ -259,6 +287,16 @@ int moe_block_norm_bwd(const moe_dims* dims, const moe_norm_cfg* cfg, int res_ty
   if ((dw_post && !w_post) || (dgate && !gate) || (dw_pre && !w_pre)) return MOE_ERR_INVALID_ARG;
   if (!ws || ws_bytes < norm_ws_bytes(*dims, *cfg)) return MOE_ERR_INVALID_ARG;
   if (!aligned(16, {dn, dres_out, y, u, w_post, gate, w_pre, dy, dres, dw_post, dgate, dw_pre, ws}))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t cells = dims->T * dims->d, row = dims->d * 4, size = res_type == MOE_F32 ? 4 : 2;
+  const int64_t gates = cfg->seq_len && dims->T ? (dims->T - 1) / cfg->seq_len + 1 : 1;
+  const Span sdn = {dn, cells * 2}, sdu = {dres_out, cells * size}, sy = {y, cells * 2},
+             su = {u, cells * size}, sdy = {dy, cells * 2}, sdres = {dres, cells * size},
+             post = {w_post, row}, sgate = {gate, gates * row}, pre = {w_pre, row};
+  if (clash({sdy, sdres}, {sdn, sdu, sy, su}, true) ||
+      clash({sdy, sdres, {dw_post, row}, {dgate, gates * row}, {dw_pre, row}},
+            {post, sgate, pre}) ||
+      clash({{dw_post, row}, {dgate, gates * row}, {dw_pre, row}}, {sdn, sdu, sy, su}))
     return MOE_ERR_INVALID_ARG;
   NormArgs a{};
   a.y = y;

@@ -573,8 +573,8 @@ typedef struct moe_route_cfg {
  * Out:
  *   topk_idx [T, k] int32, topk_w [T, k] f32
  *   probs    [T, E]  f32  affinities that sum to 1 over a token's experts: p for
- *                    softmax, p / sum_e p for sigmoid (may be NULL); must not
- *                    overlap logits
+ *                    softmax, p / sum_e p for sigmoid (may be NULL)
+ * No output may overlap an input or another output.
  * The choice is the one that 64-bit arithmetic makes on these logits; equal
  * scores go to the lower expert (equal group scores to the lower group).
  * Without a bias the experts rank by their logits.  A logit of -inf takes an
@@ -601,8 +601,8 @@ int moe_route_topk(const moe_dims* dims, const moe_route_cfg* cfg, int logits_ty
  *   logits   [T, E]  as given to the forward (logits_type)
  *   topk_idx, topk_w [T, k]  the forward's outputs; dw [T, k] f32
  *   seq_grad [ceil(T / seq_len), E] f32 (may be NULL: seq_len is not used)
- * Out: dlogits [T, E] of logits_type, not overlapping logits.  A topk_idx entry outside [0, E) is
- * skipped.  The same inputs give the same bits. */
+ * Out: dlogits [T, E] of logits_type, not overlapping an input.  A topk_idx entry
+ * outside [0, E) is skipped.  The same inputs give the same bits. */
 int moe_route_bwd(const moe_dims* dims, const moe_route_cfg* cfg, int logits_type,
                   const void* logits, const int32_t* topk_idx, const float* topk_w,
                   const float* dw, const float* seq_grad, int64_t seq_len, void* dlogits,
@@ -644,8 +644,10 @@ typedef struct moe_norm_cfg {
  *   w_post, w_pre [d] f32; gate [max(1, ceil(T / seq_len)), d] f32 (one row where
  *                seq_len = 0)
  * Out:
- *   res_out [T, d] res_type = u (may be res itself)
+ *   res_out [T, d] res_type = u
  *   n     [T, d] bf16, the next block's input; NULL with w_pre NULL: no pre-norm
+ * An output may be y or res itself, where those have its type (res_out usually is
+ * res); outputs and inputs may not overlap otherwise.
  * n is computed from u before u is rounded to res_type.  FP32 throughout: |y| and
  * |u| below 1e18.  Requires d <= 16384 and 16-byte aligned tensors. */
 int moe_block_norm(const moe_dims* dims, const moe_norm_cfg* cfg, int res_type, const void* y,
@@ -670,7 +672,8 @@ size_t moe_norm_workspace_size(const moe_dims* dims, const moe_norm_cfg* cfg);
  *   u     [T, d] res_type, the forward's res_out (res itself when y was NULL); may be
  *         NULL when dn is
  * Out:
- *   dy    [T, d] bf16; dres [T, d] res_type (may be dres_out itself)
+ *   dy    [T, d] bf16; dres [T, d] res_type; each may be dn, dres_out, y or u itself,
+ *         where those have its type; outputs and inputs may not overlap otherwise
  *   dw_post, dw_pre [d] f32, dgate as gate, f32: written, or added to when
  *         accumulate != 0; each may be NULL (not wanted)
  * FP32 throughout: |y|, |beta gate w_post y|, |u|, |dn w_pre| and |dres_out| below 1e18.

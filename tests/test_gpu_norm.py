@@ -295,3 +295,24 @@ def test_backward_of_large_and_small_rows(su, sy, sdn, eps, d, rt):
         v, mag = ref[k]
         tol = E * mag if k in ("dy", "dres") else (E + (T / 64 + 64) * U) * mag
         within(o[k], v, tol + HALF[o[k].dtype] * (v.abs() + tol) + ref64.TINY[o[k].dtype], k)
+
+
+@pytest.mark.parametrize("rt", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T,d", [(700, 192), (333, 4160), (20, 16384)])
+def test_outputs_in_the_place_of_inputs(T, d, rt):
+    i = inputs(T, d, rt, 1)
+    cfg = moe.MoeNormCfg.of(EPS, 0.9, 0.7)
+    dm, u, n = fwd(i, cfg)
+    y, res = i["y"].clone(), i["res"].clone()
+    moe.moe_block_norm(dm, cfg, y, res, i["w_post"], i["gate"], i["w_pre"], res, y)
+    assert torch.equal(y, n) and torch.equal(res, u)
+    o = bwd(i, cfg)
+    ws = torch.empty(moe.moe_norm_workspace_size(dm, cfg), dtype=torch.uint8, device="cuda")
+    for dy_over, dres_over in itertools.product(("y", "dn"), ("du", "res")):
+        c = {k: i[k].clone() for k in ("y", "dn", "du", "res")}
+        w = {k: torch.empty_like(o[k]) for k in ("dw_post", "dgate", "dw_pre")}
+        moe.moe_block_norm_bwd(dm, cfg, c["dn"], c["du"], c["y"], c["res"], i["w_post"], i["gate"],
+                               i["w_pre"], c[dy_over], c[dres_over], w["dw_post"], w["dgate"],
+                               w["dw_pre"], 0, ws)
+        assert torch.equal(c[dy_over], o["dy"]) and torch.equal(c[dres_over], o["dres"])
+        assert all(torch.equal(w[k], o[k]) for k in w)

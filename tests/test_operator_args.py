@@ -281,3 +281,55 @@ def test_first_calls_of_two_threads_find_a_whole_table(monkeypatch):
 
     monkeypatch.setattr(_lib, "_TYPES", Table())
     assert _lib._types()[torch.bfloat16] == moe.MOE_BF16 and _lib._TYPES
+
+
+def _at(i, n=0):
+    return ctypes.c_void_p((i << 20) + n)      # addresses a MB apart
+
+
+def test_routing_refuses_outputs_over_what_other_tokens_read():
+    L, cfg = _lib.load(), ctypes.byref(moe.MoeRouteCfg.of())
+    T, E, k = 64, 8, 2
+    dm = dims(T=T, E=E, k=k)
+    sizes = dict(logits=T * E * 4, bias=E * 4, idx=T * k * 4, w=T * k * 4, probs=T * E * 4)
+    names = list(sizes)
+    for out in ("idx", "w", "probs"):
+        for other in names:
+            if other == out:
+                continue
+            for off in (0, sizes[other] - 4, 4 - sizes[out]):     # over it, its end, its start
+                p = {n: _at(i + 1) for i, n in enumerate(names)}
+                p[out] = _at(names.index(other) + 1, off)
+                assert L.moe_route_topk(dm, cfg, 0, *(p[n] for n in names), NUL) == INVALID, \
+                    (out, other, off)
+    sizes = dict(logits=T * E * 4, idx=T * k * 4, w=T * k * 4, dw=T * k * 4, sg=8 * E * 4)
+    names = list(sizes)
+    for i, other in enumerate(names):
+        for off in (0, sizes[other] - 4, 4 - T * E * 4):
+            p = [_at(j + 1) for j in range(5)]
+            assert L.moe_route_bwd(dm, cfg, 0, *p, 8, _at(i + 1, off), NUL) == INVALID, (other, off)
+
+
+def test_norms_refuse_outputs_over_what_other_rows_read():
+    L = _lib.load()
+    T, d = 64, 128
+    dm, cfg = dims(T=T, d=d), ctypes.byref(moe.MoeNormCfg.of(seq_len=8))
+    rows, row = T * d * 2, d * 4
+    f = dict(y=rows, res=rows, wp=row, g=8 * row, w=row, out=rows, n=rows)
+    b = dict(dn=rows, du=rows, y=rows, u=rows, wp=row, g=8 * row, w=row, dy=rows, dres=rows,
+             dwp=row, dg=8 * row, dw=row)
+    for sizes, outs, call in (
+            (f, ("out", "n"), lambda p: L.moe_block_norm(dm, cfg, 1, *p, NUL)),
+            (b, ("dy", "dres", "dwp", "dg", "dw"),
+             lambda p: L.moe_block_norm_bwd(dm, cfg, 1, *p, 0, _at(40), BIG, NUL))):
+        names = list(sizes)
+        for out in outs:
+            for other in names:
+                if other == out:
+                    continue
+                # an input of the same shape may be the output itself
+                same = sizes[other] == sizes[out] == rows and other not in outs
+                for off in (0, sizes[other] - 16, 16 - sizes[out])[1 if same else 0:]:
+                    p = {n: _at(i + 1) for i, n in enumerate(names)}
+                    p[out] = _at(names.index(other) + 1, off)
+                    assert call(list(p.values())) == INVALID, (out, other, off)
