@@ -9,6 +9,7 @@ following a bad entry; loaded instead of libmoe.so when MOE_LIB_DEBUG=1), and wi
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -19,6 +20,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe.so")
 BIND = os.path.join(HERE, "_bind.so")
+BIND_ABI = os.path.join(HERE, "_bind.abi")  # the Python and torch that _bind.so is built for
 LIB_DEBUG = os.path.join(HERE, "libmoe_debug.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
@@ -77,10 +79,25 @@ def _build_one(lib: str, extra, force: bool, verbose: bool):
     os.replace(tmp, lib)
 
 
+def _bind_abi() -> str:
+    """What _bind.so is built against besides its sources."""
+    return f"{sys.implementation.cache_tag} torch {importlib.metadata.version('torch')}"
+
+
+def bind_stale() -> bool:
+    newest = max(map(os.path.getmtime, (os.path.join(CSRC, "bind.cpp"),
+                                        os.path.join(INCLUDE, "moe.h"), os.path.abspath(__file__))))
+    if not os.path.exists(BIND) or os.path.getmtime(BIND) < newest:
+        return True
+    try:
+        with open(BIND_ABI) as f:
+            return f.read() != _bind_abi()
+    except OSError:
+        return True
+
+
 def _build_bind(force: bool, verbose: bool):
-    src, header = os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "moe.h")
-    newest = max(map(os.path.getmtime, (src, header, os.path.abspath(__file__))))
-    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= newest:
+    if not force and not bind_stale():
         return
     import sysconfig
 
@@ -90,12 +107,14 @@ def _build_bind(force: bool, verbose: bool):
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
-           src, "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu",
-           "-lc10"]
+           os.path.join(CSRC, "bind.cpp"), "-o", tmp, "-L", os.path.join(home, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, BIND)
+    with open(BIND_ABI, "w") as f:
+        f.write(_bind_abi())
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = True) -> str:

@@ -333,3 +333,15 @@ def test_norms_refuse_outputs_over_what_other_rows_read():
                     p = {n: _at(i + 1) for i, n in enumerate(names)}
                     p[out] = _at(names.index(other) + 1, off)
                     assert call(list(p.values())) == INVALID, (out, other, off)
+
+
+def test_the_binding_is_built_again_for_another_torch_or_python(monkeypatch):
+    from grouped_gemm_fp32_b200 import build
+    assert not build.bind_stale()
+    with monkeypatch.context() as m:
+        m.setattr(build.importlib.metadata, "version", lambda name: "0.0.1+other")
+        assert build.bind_stale()
+    with monkeypatch.context() as m:
+        m.setattr(build.sys.implementation, "cache_tag", "cpython-399")
+        assert build.bind_stale()
+    assert not build.bind_stale()
