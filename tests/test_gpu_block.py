@@ -384,3 +384,52 @@ def test_block_refuses_an_input_that_its_backward_would_miss():
     want = layer.block_forward(other, *args, w_next=w, n=run.n_next.clone())
     got = layer.block_forward(run, *args, w_next=w, n=run.n_next)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("W,E,k", [(2, 16, 4), (4, 32, 6)])
+def test_emulated_expert_parallel_ranks_with_another_router(W, E, k):
+    # every phase for every rank in turn (no kernel waits for another beside it), against the
+    # layer on the concatenated batch
+    T, S = 150, 1
+    dm, t = case(T=T, E=E, k=k, S=S, seed=43)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x, dout = [r(T, dm.d) for _ in range(W)], [r(T, dm.d) for _ in range(W)]
+    wg, bias, w1, w2 = t["wg"], t["bias"], t["w1"], t["w2"]
+    ref = layer.MoEBuffers(moe.MoeDims.of(W * T, dm.d, E, k, S, dm.I, dm.P), train=True,
+                           route=rcfg(SIGMOID))
+    layer.forward(ref, torch.cat(x), wg, bias, w1, w2)
+    layer.backward(ref, torch.cat(x), torch.cat(dout), w1, w2, wg=wg)
+    ebs = [ep.EPBuffers(dm, i, W, train=True, route=rcfg(SIGMOID)) for i in range(W)]
+    ep.connect_emulated(ebs)
+    El = E // W
+    wl = [[torch.cat([w[i * El:(i + 1) * El], w[E:]]).contiguous() for w in (w1, w2)]
+          for i in range(W)]
+    for i, eb in enumerate(ebs):
+        ep.route(eb, x[i], wg, bias)
+    table = torch.stack([eb.full.counts for eb in ebs])
+    for eb in ebs:
+        eb.counts_all.copy_(table)
+        ep.plan(eb)
+    for i, eb in enumerate(ebs):
+        ep.dispatch(eb, x[i])
+    for i, eb in enumerate(ebs):
+        ep.experts_forward(eb, x[i], *wl[i])
+    out = [ep.combine(eb).clone() for eb in ebs]
+    for i, eb in enumerate(ebs):
+        ep.backward_dispatch(eb, dout[i])
+    for i, eb in enumerate(ebs):
+        ep.experts_backward(eb, x[i], dout[i], *wl[i])
+    dx = [ep.unpermute_and_router(eb, x[i], wg).clone() for i, eb in enumerate(ebs)]
+    torch.cuda.synchronize()
+    assert all(ep.status(eb) == 0 for eb in ebs)
+    full = lambda n: torch.cat([getattr(eb.full, n) for eb in ebs])  # noqa: E731
+    # a token's logits and choice are the same whichever rank it is on
+    assert torch.equal(full("logits"), ref.logits) and torch.equal(full("topk_idx"), ref.topk_idx)
+    assert torch.equal(full("topk_w"), ref.topk_w)
+    assert rel(torch.cat(out), ref.out) <= ROW_TOL and rel(torch.cat(dx), ref.dx) <= ROW_TOL
+    assert rel(full("dlogits"), ref.dlogits) <= DW_TOL
+    assert rel(sum(eb.full.dwg.double() for eb in ebs), ref.dwg) <= DW_TOL
+    for n in ("dw1", "dw2"):
+        got = torch.cat([getattr(eb.loc, n)[:El] for eb in ebs])
+        assert rel(got, getattr(ref, n)[:E]) <= DW_TOL

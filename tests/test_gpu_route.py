@@ -483,3 +483,33 @@ def test_a_group_of_one_infinite_and_masked_experts_ranks_last(E, G, T, score):
         assert torch.equal(idx, ridx), one
         ref64.within(w, rw, 2 * (24 + 16) * 2.0 ** -23 * rw, "weights")
         check(y, c, cfg | dict(group_top=1))
+
+
+@pytest.mark.parametrize("T,d,E", [(1, 64, 8), (300, 128, 8), (1000, 192, 96), (129, 256, 256),
+                                   (2100, 320, 128)])
+def test_gate_bwd_element_by_element(T, d, E):
+    """Each element against the magnitude of its own terms.  The operands are split exactly
+    into three bf16 planes, whose magnitudes add up to less than 1.02 of the value; a matrix
+    instruction adds 16 products to the accumulator, cutting at most three steps of 2^-23 of
+    the terms so far; dX drops three pairs of planes below 2^-24 each and is rounded once to
+    bf16; dWg adds up to 64 partial sums."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, wg, dl = r(T, d).bfloat16(), 0.05 * r(E, d), r(T, E) * torch.exp(2 * r(T, 1))
+    dl[::7] = 0.0
+    dm = moe.MoeDims.of(T, d, E, 1, 0, 64, 64)
+    ws = torch.zeros(moe.moe_workspace_size(dm), dtype=torch.uint8, device="cuda")
+    dx0 = (0.01 * r(T, d)).bfloat16()
+    blocks = lambda n: -(-n // 64) * 4  # noqa: E731  instructions of one plane pair
+    for acc in (0, 1):
+        dx, dwg = dx0.clone(), r(E, d)
+        w0 = dwg.double() if acc else torch.zeros(E, d, dtype=torch.float64, device="cuda")
+        moe.moe_gate_bwd(dm, x, wg, dl, dx, dwg, acc, ws)
+        rx = dx0.double() + dl.double() @ wg.double()
+        mag = dx0.double().abs() + dl.double().abs() @ wg.double().abs()
+        tol = (18 * blocks(E) + 4) * 1.02 * 2.0 ** -23 * mag
+        ref64.within(dx, rx, tol + 2.0 ** -8 * (rx.abs() + tol), "dx")
+        rw = w0 + dl.double().T @ x.double()
+        mag = w0.abs() + dl.double().abs().T @ x.double().abs()
+        ref64.within(dwg, rw, (9 * blocks(T) + 66) * 1.02 * 2.0 ** -23 * mag, "dwg")
+    assert moe.moe_get_device_status(ws) == 0
