@@ -47,10 +47,14 @@ constexpr int NV = 8;             // columns per vector
 // the arithmetic, to fill it).  Two vectors a thread halve what a row costs beside its
 // arithmetic and double the rows in work on an SM.  Forward that pays from two vectors a
 // lane on: 16384 rows of 512 columns 10.4 instead of 15.4 us, 1024 22 instead of 30, 1536 39
-// instead of 56.  The backward has more arithmetic and registers: 1536 columns 65 instead of
-// 73 us, 1984 84 instead of 90, but 768 45 instead of 42, and 2000 rows of 1024 16 instead
-// of 13; and more CTAs, of which few rows feel the column sums: 2000 rows of 1984 18.7
-// instead of 20.6 us, 777 18.1 instead of 16.3.
+// instead of 56.  The backward has more arithmetic and registers, and more CTAs, of which few
+// rows, and rows of many gates, feel the column sums: up to 1024 columns one vector is faster
+// at any number of rows (16384 of 768 42 instead of 45 us, 2000 of 1024 13 instead of 16).  To
+// 2048 columns the wider the rows the fewer of them it takes; one vector against two, a gate
+// row for all: 1088 columns 11.7 / 13.2 us for 1000 rows, 13.9 / 14.9 for 2000, 60 / 59 for
+// 16384; 1536 columns 13.5 / 14.0, 18.7 / 16.0, 71 / 58; 2048 columns 15.8 / 14.3, 19.2 / 16.7,
+// 82 / 76 (11.3 / 13.6 for 500).  With a gate row for 130 tokens one vector stays ahead: 2048
+// columns 13.8 / 17.2, 19.6 / 25.3, 95 / 145.  1024 rows stand between the two.
 struct Shape {
   int v, threads, per_sm;
 };

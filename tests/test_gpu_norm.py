@@ -316,3 +316,10 @@ def test_outputs_in_the_place_of_inputs(T, d, rt):
                                w["dw_pre"], 0, ws)
         assert torch.equal(c[dy_over], o["dy"]) and torch.equal(c[dres_over], o["dres"])
         assert all(torch.equal(w[k], o[k]) for k in w)
+
+
+@pytest.mark.parametrize("rt", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T,d", [(300, 1088), (1023, 1088), (1024, 1088), (1023, 1536), (1024, 1536),
+                                 (1023, 2048), (1024, 2048), (1, 2048), (200, 1984)])
+def test_backward_on_both_sides_of_one_vector_a_thread(T, d, rt):
+    check_bwd(inputs(T, d, rt, -(-T // 100)), (1.0, 0.7, 100))
