@@ -1232,7 +1232,8 @@ __global__ void __launch_bounds__(RT_WARPS * 32, EPL == 8 ? 8 : 10)
 #pragma unroll
     for (int i = 0; i < 5; ++i) sum[i] += __shfl_xor_sync(FULL, sum[i], o);
   const float z = sum[3], rz = z == 0.0f ? 0.0f : quick_rcp(z);
-  bool bad = !SOFT && SEQ && z < RT_SMALL_ALL;
+  // a pick too near the subnormal numbers: its gradient may be an ordinary number
+  bool bad = (!SOFT && SEQ && z < RT_SMALL_ALL) || (ok && pe < RT_TINY);
   const bool any = (__ballot_sync(FULL, ok) & ALL << base) != 0;
   const float unit = SOFT ? rz : 1.0f;  // of p
   float d = a.scale * dwj, cp = a.scale * sum[2] * unit;  // cp: sum of p dp over the picks

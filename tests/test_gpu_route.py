@@ -513,3 +513,38 @@ def test_gate_bwd_element_by_element(T, d, E):
         mag = w0.abs() + dl.double().abs().T @ x.double().abs()
         ref64.within(dwg, rw, (9 * blocks(T) + 66) * 1.02 * 2.0 ** -23 * mag, "dwg")
     assert moe.moe_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("T", [60, MANY])
+@pytest.mark.parametrize("E", [64, 128, 256])
+def test_bwd_of_picks_far_below_the_others(E, T, score):
+    # the bias chooses experts whose affinities are subnormal numbers of FP32 beside small ones:
+    # their gradients are ordinary numbers
+    x, b, cfg = make(T, E, 4, 31, score=score, scale=1.5)
+    if score == SG:
+        x = x - 60.0
+    b = torch.zeros_like(b)
+    for j, e in enumerate((3, E // 2, E - 1, 17)):
+        b[e] = 2.0 - 0.1 * j
+        x[:, e] = x[:, e] * 0.5 - (30.0, 90.0, 95.0, 45.0)[j] + (0.0 if score == SM else 60.0)
+    dm, rc, idx, w, _ = check(x, b, cfg)
+    dw = torch.randn(T, 4, generator=torch.Generator(device="cuda").manual_seed(T), device="cuda")
+    bwd_check(x, idx, w, dw, cfg, rc, dm)
+    sg = torch.randn(-(-T // 50), E, device="cuda")
+    if score == SM:
+        bwd_check(x, idx, w, dw, cfg, rc, dm, sg, 50)
+
+
+@pytest.mark.parametrize("T", [60, MANY])
+@pytest.mark.parametrize("E", [64, 128, 256])
+def test_bwd_of_picks_of_tiny_sigmoids(E, T):
+    x, b, cfg = make(T, E, 4, 32, score=SG, scale=1.5)
+    b = torch.zeros_like(b)
+    for j, e in enumerate((3, E // 2, E - 1, 17)):
+        b[e] = 2.0 - 0.1 * j
+        x[:, e] = x[:, e] * 0.5 - (30.0, 90.0, 97.0, 75.0)[j]
+    dm, rc, idx, w, _ = check(x, b, cfg)
+    dw = torch.randn(T, 4, generator=torch.Generator(device="cuda").manual_seed(T), device="cuda")
+    bwd_check(x, idx, w, dw, cfg, rc, dm)
+    bwd_check(x, idx, w, dw, cfg, rc, dm, torch.randn(-(-T // 50), E, device="cuda"), 50)
