@@ -657,9 +657,9 @@ __device__ __noinline__ bool refine(const RouteArgs& a, int64_t t, float m, floa
   const float sum = warp_sum(p);
   if (!(sum > RT_SMALL_SUM) || __any_sync(FULL, pick && p < RT_TINY)) return false;
   if (pick) {
-    const float f = a.renorm ? a.scale * quick_rcp(sum) : a.scale * (a.softmax ? rz : 1.0f);
+    const float f = a.renorm ? quick_rcp(sum) : a.softmax ? rz : 1.0f;
     a.idx[t * a.k + rank] = c;
-    a.w[t * a.k + rank] = p * f;
+    a.w[t * a.k + rank] = a.scale * (p * f);
   }
   return true;
 }
@@ -805,10 +805,9 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, RouteS
   if (some && pe < RT_TINY) bad |= load1(row + e) - m > -140.0f;
   if (__any_sync(FULL, bad)) return RT_STOP;
   if (mine) {
-    const float f = a.renorm ? (sum == 0.0f ? 0.0f : a.scale * quick_rcp(sum))
-                             : a.scale * (SOFT ? rz : 1.0f);
+    const float f = a.renorm ? (sum == 0.0f ? 0.0f : quick_rcp(sum)) : (SOFT ? rz : 1.0f);
     a.idx[t * a.k + lane] = e;
-    a.w[t * a.k + lane] = pe * f;
+    a.w[t * a.k + lane] = a.scale * (pe * f);
   }
   return __any_sync(FULL, near) ? RT_NEAR : RT_DONE;
 }
@@ -1040,10 +1039,9 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8)
   if (some && pe < RT_TINY) bad |= load1(row + e) - m > -140.0f;
   const uint32_t stopped = __ballot_sync(FULL, bad && real);
   if (mine && real && !(stopped & ALL << base)) {
-    const float f = a.renorm ? (sum == 0.0f ? 0.0f : a.scale * quick_rcp(sum))
-                             : a.scale * (SOFT ? rz : 1.0f);
+    const float f = a.renorm ? (sum == 0.0f ? 0.0f : quick_rcp(sum)) : (SOFT ? rz : 1.0f);
     a.idx[t * a.k + l] = e;
-    a.w[t * a.k + l] = pe * f;
+    a.w[t * a.k + l] = a.scale * (pe * f);
   }
   const uint32_t nears = __ballot_sync(FULL, near && real);
   if ((stopped | nears) == 0) return;
@@ -1236,13 +1234,14 @@ __global__ void __launch_bounds__(RT_WARPS * 32, EPL == 8 ? 8 : 10)
   bool bad = (!SOFT && SEQ && z < RT_SMALL_ALL) || (ok && pe < RT_TINY);
   const bool any = (__ballot_sync(FULL, ok) & ALL << base) != 0;
   const float unit = SOFT ? rz : 1.0f;  // of p
-  float d = a.scale * dwj, cp = a.scale * sum[2] * unit;  // cp: sum of p dp over the picks
+  float d = a.scale * dwj, cp = a.scale * (sum[2] * unit);  // cp: sum of p dp over the picks
   if (a.renorm) {
     bad |= any && sum[0] < RT_SMALL_SUM;
     const float r = any ? 1.0f / sum[0] : 0.0f;  // 1 / sum of the picks' p z
     d = (d - sum[1]) * r * (SOFT ? z : 1.0f);
-    cp = a.scale * sum[2] * r - (any ? sum[1] : 0.0f);
+    cp = a.scale * (sum[2] * r) - (any ? sum[1] : 0.0f);
   }
+  bad |= ok && fabsf(d) == INFINITY;  // the factor over a small sum
   if (twice) {  // both terms, in the picks' order
     const unsigned same = __match_any_sync(FULL, ok ? base << 16 | e : -1 - lane);
     float v = 0.0f;

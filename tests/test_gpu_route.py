@@ -548,3 +548,24 @@ def test_bwd_of_picks_of_tiny_sigmoids(E, T):
     dw = torch.randn(T, 4, generator=torch.Generator(device="cuda").manual_seed(T), device="cuda")
     bwd_check(x, idx, w, dw, cfg, rc, dm)
     bwd_check(x, idx, w, dw, cfg, rc, dm, torch.randn(-(-T // 50), E, device="cuda"), 50)
+
+
+@pytest.mark.parametrize("score", [SM, SG])
+@pytest.mark.parametrize("T", [60, MANY])
+@pytest.mark.parametrize("E", [64, 128, 256])
+def test_factors_of_any_size(E, T, score):
+    # scale / (sum of the picks) leaves FP32 where the weights do not, at either end
+    for scale in (1e32, -1e32, 1e-32):
+        x, b, cfg = make(T, E, 4, 33, score=score, scale=scale)
+        b = torch.zeros_like(b)
+        for j, e in enumerate((3, E // 2, E - 1, 17)):
+            b[e] = 2.0 - 0.1 * j
+            x[:, e] = x[:, e] * 0.5 - 36.0
+        dm, rc, idx, w, _ = call(x, b, cfg)
+        ridx, rw, _, _ = ref64.route(x, b, cfg)
+        assert torch.equal(idx, ridx)
+        ref64.within(w, rw, 2 * (24 + 45) * 2.0 ** -23 * rw.abs(), "weights")
+        assert w.isfinite().all() and (w != 0).all()
+        dw = torch.randn(T, 4, generator=torch.Generator(device="cuda").manual_seed(T),
+                         device="cuda")
+        bwd_check(x, idx, w, dw, cfg, rc, dm)
