@@ -149,7 +149,8 @@ static int check_route(const moe_dims* dims, const moe_route_cfg* c, int type) {
   if (c->n_group < 1 || c->topk_group < 1 || c->topk_group > c->n_group)
     return MOE_ERR_INVALID_ARG;
   if (!(c->scale - c->scale == 0.0f)) return MOE_ERR_INVALID_ARG;  // not finite
-  if (dims->E > 256 || dims->k > dims->E || dims->T * dims->k >= (int64_t(1) << 31))
+  constexpr int64_t MOST = int64_t(1) << 31;
+  if (dims->E > 256 || dims->k > dims->E || dims->T >= MOST || dims->T * dims->k >= MOST)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (dims->E % c->n_group) return MOE_ERR_UNSUPPORTED_SHAPE;
   // a group must hold group_top experts, the kept groups k of them

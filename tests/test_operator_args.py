@@ -345,3 +345,9 @@ def test_the_binding_is_built_again_for_another_torch_or_python(monkeypatch):
         m.setattr(build.sys.implementation, "cache_tag", "cpython-399")
         assert build.bind_stale()
     assert not build.bind_stale()
+
+
+def test_token_counts_whose_picks_leave_64_bits():
+    for T, k in (((1 << 62) + 4, 2), ((1 << 61) + 4, 8), (1 << 62, 4)):
+        assert route(dm=dims(T=T, k=k)) == SHAPE
+        assert route_bwd(dm=dims(T=T, k=k)) == SHAPE
