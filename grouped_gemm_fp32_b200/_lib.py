@@ -514,15 +514,38 @@ class GradList:
             a.data = _need("gradient", g, g.dtype, g.numel(), dev)
             a.out = _need("clipped gradient", o, g.dtype, g.numel(), dev)
             a.n = g.numel()
+        self.overlap = self._overlap()
+
+    def _overlap(self):
+        """What a clipping would write and another tensor of the list shares, or None."""
+        spans = []      # start, end, written, entry
+        for i, (a, g) in enumerate(zip(self.array, self.grads)):
+            size = a.n * g.element_size()
+            if size:
+                spans.append((a.out or a.data, size, True, i))
+                if a.out and a.out != a.data:
+                    spans.append((a.data, size, False, i))
+        read = written = (0, None)      # the furthest end so far, and whose it is
+        for start, size, writes, i in sorted(spans):
+            for end, j in (read, written) if writes else (written,):
+                if start < end:
+                    return f"tensors {j} and {i} overlap"
+            if writes:
+                written = max(written, (start + size, i))
+            else:
+                read = max(read, (start + size, i))
+        return None
 
     def __len__(self):
         return len(self.grads)
 
-    def on(self, dev):
-        """Its address and length, for a call on device ``dev``."""
+    def on(self, dev, clip=True):
+        """Its address and length, for a call on device ``dev`` that clips it or does not."""
         if self.device != dev and self.device is not None:
             raise ValueError(f"gradients: on device {self.device}, the current device is "
                              f"cuda:{dev}")
+        if clip and self.overlap:
+            raise ValueError(f"gradients: {self.overlap}")
         return self.address, len(self.grads)
 
 
@@ -532,7 +555,7 @@ def moe_grad_workspace_size(n_grads) -> int:
 
 def moe_grad_norm(grads, accumulate, sumsq, norm, ws, stream=None):
     at = _here(stream)
-    _ck((_bound or _bind()).grad_norm(*grads.on(at[0]), accumulate, sumsq, norm, ws, *at),
+    _ck((_bound or _bind()).grad_norm(*grads.on(at[0], False), accumulate, sumsq, norm, ws, *at),
         "moe_grad_norm")
 
 

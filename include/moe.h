@@ -692,8 +692,8 @@ int moe_block_norm_bwd(const moe_dims* dims, const moe_norm_cfg* cfg, int res_ty
  * returns; its tensors are device memory of any element-aligned address. */
 typedef struct moe_grad {
   const void* data; /* n elements (may be NULL when n = 0) */
-  void* out;        /* where the clipped elements go; NULL or data: in place.  Otherwise
-                       it must not overlap any tensor of the list */
+  void* out;        /* where the clipped elements go; NULL or data: in place.  What a
+                       clipping writes must not overlap another tensor of the list */
   int64_t n;
   int32_t type;     /* MOE_F32, MOE_BF16 or MOE_F16, of data and out */
 } moe_grad;

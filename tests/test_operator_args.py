@@ -351,3 +351,26 @@ def test_token_counts_whose_picks_leave_64_bits():
     for T, k in (((1 << 62) + 4, 2), ((1 << 61) + 4, 8), (1 << 62, 4)):
         assert route(dm=dims(T=T, k=k)) == SHAPE
         assert route_bwd(dm=dims(T=T, k=k)) == SHAPE
+
+
+def test_clipping_refuses_tensors_that_overlap_what_it_writes(monkeypatch):
+    # a tensor in the list twice would be scaled once or twice, as the CTAs come
+    _lib._types()
+    monkeypatch.setitem(_lib._TYPES, "device", lambda: -1)     # host tensors; no call is made
+    x, y = torch.zeros(100), torch.zeros(100)
+    ws = torch.zeros(8, dtype=torch.uint8)
+    bad = [([x, x], None), ([x, x[50:]], None), ([x[:60], y, x[59:]], None), ([x, y], [y, None]),
+           ([x, y], [None, x]), ([x[:50], y[:50]], [y[50:], y[50:]]), ([x[1:50]], [x[:49]])]
+    for grads, outs in bad:
+        lst = moe.GradList(grads, outs)
+        for call in (lambda: moe.moe_grad_clip(lst, 16, 1.0, None, None, 0),
+                     lambda: moe.moe_grad_clip_norm(lst, 1.0, 16, None, None, ws, 0)):
+            with pytest.raises(ValueError, match="gradients: .* overlap"):
+                call()
+        # a norm alone writes none of them: the next check answers
+        with pytest.raises(ValueError, match="sumsq"):
+            moe.moe_grad_norm(lst, 0, x, None, ws, 0)
+    for grads, outs in (([x[:50], x[50:]], None), ([x, x], [y, torch.zeros(100)]),
+                        ([x, y], [x, y]), ([x[:0], x], None), ([x, x[:0]], [y, y[10:10]])):
+        with pytest.raises(ValueError, match="sumsq"):
+            moe.moe_grad_clip(moe.GradList(grads, outs), x, 1.0, None, None, 0)
