@@ -509,31 +509,31 @@ class GradList:
         self.address = ctypes.addressof(self.array)
         # the calls read addresses: they have to be made on the tensors' device
         dev = self.device = _types()["device"]() if self.grads else None
-        for a, g, o in zip(self.array, self.grads, self.outs):
-            a.type = _kind("gradient", g, (MOE_F32, MOE_BF16, MOE_F16))
-            a.data = _need("gradient", g, g.dtype, g.numel(), dev)
-            a.out = _need("clipped gradient", o, g.dtype, g.numel(), dev)
-            a.n = g.numel()
-        self.overlap = self._overlap()
+        spans = []      # start, bytes, written, entry
+        for i, (a, g, o) in enumerate(zip(self.array, self.grads, self.outs)):
+            a.type = kind = _kind("gradient", g, (MOE_F32, MOE_BF16, MOE_F16))
+            a.n = n = g.numel()
+            a.data = data = _need("gradient", g, g.dtype, n, dev)
+            a.out = out = _need("clipped gradient", o, g.dtype, n, dev)
+            if n:
+                size = 4 * n if kind == MOE_F32 else 2 * n
+                spans.append((out or data, size, True, i))
+                if out and out != data:
+                    spans.append((data, size, False, i))
+        self.overlap = self._overlap(spans)
 
-    def _overlap(self):
+    @staticmethod
+    def _overlap(spans):
         """What a clipping would write and another tensor of the list shares, or None."""
-        spans = []      # start, end, written, entry
-        for i, (a, g) in enumerate(zip(self.array, self.grads)):
-            size = a.n * g.element_size()
-            if size:
-                spans.append((a.out or a.data, size, True, i))
-                if a.out and a.out != a.data:
-                    spans.append((a.data, size, False, i))
         read = written = (0, None)      # the furthest end so far, and whose it is
         for start, size, writes, i in sorted(spans):
             for end, j in (read, written) if writes else (written,):
                 if start < end:
                     return f"tensors {j} and {i} overlap"
-            if writes:
-                written = max(written, (start + size, i))
-            else:
-                read = max(read, (start + size, i))
+            if writes and start + size > written[0]:
+                written = (start + size, i)
+            if not writes and start + size > read[0]:
+                read = (start + size, i)
         return None
 
     def __len__(self):
