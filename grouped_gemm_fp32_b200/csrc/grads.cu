@@ -8,7 +8,8 @@
 // A launch splits its tensors into chunks of up to GL_CHUNK elements of one tensor each;
 // CTA b takes chunks b, b + gridDim, ... .  Squares are exact in 64 bits (an FP32 value's
 // square has 48 significant bits) and are added in 64 bits: no overflow, no lost small
-// elements.  Every sum runs in an order fixed by the list's sizes.
+// elements.  Every sum runs in an order fixed by the list's sizes and its tensors' addresses
+// modulo 16 (whole vectors first).
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -462,8 +463,8 @@ int launch_grad_norm(const moe_grad* g, int64_t n, int accumulate, double* sumsq
                        norm);
 }
 
-// The clipping's launches, last tensors first.  parts > 0: after the norm's, by its
-// partial sums.
+// The clipping's launches, in the list's order (each takes its own chunks from the last one
+// on).  parts > 0: after the norm's, by its partial sums.
 template <int N>
 static int clip_with(const moe_grad* g, int64_t n, const double* part, int64_t parts,
                      double* sumsq, float max_norm, float* norm, float* coef, cudaStream_t st) {

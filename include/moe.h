@@ -609,7 +609,8 @@ int moe_route_bwd(const moe_dims* dims, const moe_route_cfg* cfg, int logits_typ
                   void* stream);
 
 /* The gate's logits on their own (Passage: as moe_gate_topk: FP32 gating):
- * logits [T, E] f32 = x Wg^T, the sums that moe_gate_topk routes by, bit for bit.
+ * logits [T, E] f32 = x Wg^T, by the kernel of moe_gate_topk, which stores the
+ * sums that it would route by.
  * x [T, d] bf16, wg [E, d] f32, ws / ws_bytes and requirements as there. */
 int moe_gate_logits(const moe_dims* dims, const void* x, const float* wg, float* logits, void* ws,
                     size_t ws_bytes, void* stream);
@@ -707,7 +708,8 @@ size_t moe_grad_workspace_size(int64_t n_grads);
  *   norm  [1] f32 (device, may be NULL): sqrt(sumsq)
  * Sharded gradients: add the ranks' sumsq, then moe_grad_clip.  Elements are
  * squared and added without overflow or loss of small ones (64-bit sums), in an
- * order fixed by the list's sizes: the same list of values gives the same bits.
+ * order fixed by the list's sizes and its addresses modulo 16: the same values at
+ * the same alignments give the same bits.
  * Two calls on one workspace must not overlap on the GPU. */
 int moe_grad_norm(const moe_grad* grads, int64_t n_grads, int accumulate, double* sumsq,
                   float* norm, void* ws, size_t ws_bytes, void* stream);
