@@ -119,6 +119,28 @@ int moe_seq_balance_loss(const moe_dims* dims, int64_t seq_len, float alpha,
   return launch_seq_balance(*dims, seq_len, alpha, topk_idx, probs, loss, seq_grad, ws, stream);
 }
 
+// A tensor's bytes (NULL: none).
+struct Span {
+  const void* p;
+  int64_t n;
+};
+static bool share(const Span& a, const Span& b) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+  return p && q && a.n > 0 && b.n > 0 && p < q + (uintptr_t)b.n && q < p + (uintptr_t)a.n;
+}
+// Whether an output shares bytes with an input or with another output.  rows: with an input
+// that is the very same tensor it may (a row is read before it is written).
+static bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins,
+                  bool rows = false) {
+  for (const Span& o : outs) {
+    for (const Span& i : ins)
+      if (share(o, i) && !(rows && o.p == i.p && o.n == i.n)) return true;
+    for (const Span& u : outs)
+      if (&u < &o && share(o, u)) return true;
+  }
+  return false;
+}
+
 int moe_gate_logits(const moe_dims* dims, const void* x, const float* wg, float* logits, void* ws,
                     size_t ws_bytes, void* stream) {
   int rc = check_shape(dims, false);
@@ -126,6 +148,9 @@ int moe_gate_logits(const moe_dims* dims, const void* x, const float* wg, float*
   if (dims->E % 8) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!ws || ws_bytes < ws_layout(*dims).total) return MOE_ERR_INVALID_ARG;
   if (dims->T > 0 && (!x || !wg || !logits)) return MOE_ERR_INVALID_ARG;
+  const int64_t rows = dims->T * dims->d * 2, gate = (int64_t)dims->E * dims->d * 4;
+  if (clash({{logits, dims->T * dims->E * 4}}, {{x, rows}, {wg, gate}}))
+    return MOE_ERR_INVALID_ARG;
   return launch_gate_topk(*dims, x, wg, nullptr, nullptr, nullptr, nullptr, logits, ws, stream);
 }
 
@@ -136,6 +161,9 @@ int moe_gate_bwd(const moe_dims* dims, const void* x, const float* wg, const flo
   if (dims->E % 8) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!ws || ws_bytes < ws_layout(*dims).total || !wg || !dwg) return MOE_ERR_INVALID_ARG;
   if (dims->T > 0 && (!x || !dlogits || !dx)) return MOE_ERR_INVALID_ARG;
+  const int64_t rows = dims->T * dims->d * 2, gate = (int64_t)dims->E * dims->d * 4;
+  if (clash({{dx, rows}, {dwg, gate}}, {{x, rows}, {wg, gate}, {dlogits, dims->T * dims->E * 4}}))
+    return MOE_ERR_INVALID_ARG;
   return launch_gate_bwd(*dims, x, wg, dlogits, dx, dwg, accumulate ? 1 : 0, ws, stream);
 }
 
@@ -165,28 +193,6 @@ static bool aligned(uintptr_t bytes, std::initializer_list<const void*> p) {
   for (const void* q : p)
     if (reinterpret_cast<uintptr_t>(q) & (bytes - 1)) return false;
   return true;
-}
-
-// A tensor's bytes (NULL: none).
-struct Span {
-  const void* p;
-  int64_t n;
-};
-static bool share(const Span& a, const Span& b) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
-  return p && q && a.n > 0 && b.n > 0 && p < q + (uintptr_t)b.n && q < p + (uintptr_t)a.n;
-}
-// Whether an output shares bytes with an input or with another output.  rows: with an input
-// that is the very same tensor it may (a row is read before it is written).
-static bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins,
-                  bool rows = false) {
-  for (const Span& o : outs) {
-    for (const Span& i : ins)
-      if (share(o, i) && !(rows && o.p == i.p && o.n == i.n)) return true;
-    for (const Span& u : outs)
-      if (&u < &o && share(o, u)) return true;
-  }
-  return false;
 }
 
 int moe_route_topk(const moe_dims* dims, const moe_route_cfg* cfg, int logits_type,

@@ -610,7 +610,7 @@ int moe_route_bwd(const moe_dims* dims, const moe_route_cfg* cfg, int logits_typ
 
 /* The gate's logits on their own (Passage: as moe_gate_topk: FP32 gating):
  * logits [T, E] f32 = x Wg^T, by the kernel of moe_gate_topk, which stores the
- * sums that it would route by.
+ * sums that it would route by; logits may not overlap x or wg.
  * x [T, d] bf16, wg [E, d] f32, ws / ws_bytes and requirements as there. */
 int moe_gate_logits(const moe_dims* dims, const void* x, const float* wg, float* logits, void* ws,
                     size_t ws_bytes, void* stream);
@@ -618,7 +618,8 @@ int moe_gate_logits(const moe_dims* dims, const void* x, const float* wg, float*
 /* The gate's gradients from those of its logits (Passage: as moe_router_bwd,
  * whose two GEMMs these are): dx += dlogits Wg, dwg (+)= dlogits^T x.
  *   dlogits [T, E] f32; dx [T, d] bf16 read-modify-write; dwg [E, d] f32 written,
- *   or added to when accumulate != 0; ws / ws_bytes and requirements as there. */
+ *   or added to when accumulate != 0; neither may overlap another operand;
+ *   ws / ws_bytes and requirements as there. */
 int moe_gate_bwd(const moe_dims* dims, const void* x, const float* wg, const float* dlogits,
                  void* dx, float* dwg, int accumulate, void* ws, size_t ws_bytes, void* stream);
 

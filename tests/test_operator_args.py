@@ -374,3 +374,24 @@ def test_clipping_refuses_tensors_that_overlap_what_it_writes(monkeypatch):
                         ([x, y], [x, y]), ([x[:0], x], None), ([x, x[:0]], [y, y[10:10]])):
         with pytest.raises(ValueError, match="sumsq"):
             moe.moe_grad_clip(moe.GradList(grads, outs), x, 1.0, None, None, 0)
+
+
+def test_gate_calls_refuse_outputs_over_their_operands():
+    L = _lib.load()
+    T, d, E = 64, 128, 8
+    dm = dims(T=T, d=d, E=E)
+    sizes = dict(x=T * d * 2, wg=E * d * 4, logits=T * E * 4)
+    for other in ("x", "wg"):
+        for off in (0, sizes[other] - 16, 16 - sizes["logits"]):
+            p = [_at(1), _at(2), _at(1 + ("x", "wg").index(other), off)]
+            assert L.moe_gate_logits(dm, *p, _at(9), BIG, NUL) == INVALID, (other, off)
+    sizes = dict(x=T * d * 2, wg=E * d * 4, dl=T * E * 4, dx=T * d * 2, dwg=E * d * 4)
+    names = list(sizes)
+    for out in ("dx", "dwg"):
+        for other in names:
+            for off in (0, sizes[other] - 16, 16 - sizes[out]):
+                if other == out:
+                    continue
+                p = [_at(i + 1) for i in range(5)]
+                p[names.index(out)] = _at(names.index(other) + 1, off)
+                assert L.moe_gate_bwd(dm, *p, 0, _at(9), BIG, NUL) == INVALID, (out, other, off)
